@@ -321,6 +321,58 @@ moe_status moe_combine_partial(const uint16_t* y, const int32_t* inv, const int3
                                const uint16_t* shared_y, int32_t T, int32_t k, int32_t H,
                                uint16_t* out, void* stream);
 
+/* ---------------------------------------------------------------- the block around the layer
+ * The calls a transformer block makes before the experts: its norm, with the residual's addition
+ * and the FP8 activations the A8 calls take, and the router's product, whose scores moe_route
+ * ranks [A2 4.1; OSDI DSLP section "gating"]. */
+
+/* RMS norm of rows of K values, with the residual added first:
+ *     s = bf16_rne(x + residual)   (s = x when residual is NULL)
+ *     v = s / sqrt(mean(s^2) + eps) * weight, computed in double and rounded to fp32
+ *     y = bf16_rne(v);  codes, exps = v in E4M3FN 128-blocks with power-of-two scales, by
+ *     moe_quantize_act's rule (of the fp32 v, so without y's rounding in between)
+ *   x, residual : bf16 [rows][K]; residual may be NULL.      weight : bf16 [K].
+ *   sum_out     : bf16 [rows][K] out, s; NULL when not wanted; requires a residual.
+ *   y           : bf16 [rows][K] out, or NULL.
+ *   codes, exps : uint8 [rows][K] and int8 [rows][exp_pitch] out as moe_quantize_act writes them
+ *                 (exp_pitch >= K/128; the rest of an exps row is not written), or both NULL.
+ * sum_out may be the same pointer as x or as residual (the residual stream updated in place); no
+ * other buffers may alias.  Values are finite by contract; otherwise they only reach outputs of
+ * their own row: a NaN or an infinity of s makes v NaN in its own place (a NaN the whole row), a
+ * NaN v takes no part in its block's exponent, and a v that is NaN or infinite has an E4M3FN
+ * NaN as its code.
+ * Errors: INVALID_ARG for rows < 0, K < 1, an eps that is not positive and finite, one of
+ * codes/exps without the other, exp_pitch < K/128 with codes, neither y nor codes, sum_out without
+ * residual, null or unaligned pointers; UNSUPPORTED when K is not a multiple of 8 (of 128 with
+ * codes) or K > MOE_MAX_DIM.  rows == 0 enqueues nothing. */
+moe_status moe_rmsnorm_quantize_act(const uint16_t* x, const uint16_t* residual,
+                                    const uint16_t* weight, int32_t rows, int32_t K, float eps,
+                                    uint16_t* sum_out, uint16_t* y, uint8_t* codes, int8_t* exps,
+                                    int32_t exp_pitch, void* stream);
+
+typedef enum { MOE_ROUTER_W_BF16 = 0, MOE_ROUTER_W_F32 = 1 } moe_router_wdtype;
+
+/* Bytes of device workspace moe_router_scores needs (host output; for either weight type): 0 up to
+ * 16 tokens and where the output tiles alone fill the chip, else fp32 partial scores of the parts
+ * K is split into.  Errors as for moe_router_scores, plus INVALID_ARG for a null `bytes`. */
+moe_status moe_router_scores_workspace_size(int32_t T, int32_t H, int32_t E, size_t* bytes);
+
+/* Router scores: scores[t][e] = sum_h x[t][h] w[e][h], products exact, sums in fp32, in an order
+ * that depends on the sizes alone (equal inputs give equal bits).
+ *   x      : bf16 [T][H].
+ *   w      : [E][H], bf16 (MOE_ROUTER_W_BF16) or fp32 (MOE_ROUTER_W_F32; all 24 significand bits
+ *            count).
+ *   scores : fp32 [T][E] out, as moe_route takes them.
+ *   ws     : device workspace of ws_bytes >= moe_router_scores_workspace_size bytes, 16-byte
+ *            aligned (may be NULL when that size is 0), not used by other work until the enqueued
+ *            launches complete.
+ * Errors: INVALID_ARG for T < 0, H < 1, E < 1, an unknown w_dtype, null or unaligned pointers;
+ * UNSUPPORTED when H is not a multiple of 8, H > MOE_MAX_DIM, E > MOE_MAX_EXPERTS or T*E >= 2^31;
+ * WORKSPACE when ws is NULL or too small. */
+moe_status moe_router_scores(const uint16_t* x, int32_t T, int32_t H, const void* w,
+                             int32_t w_dtype, int32_t E, float* scores, void* ws, size_t ws_bytes,
+                             void* stream);
+
 /* Static, human-readable name of a status code. */
 const char* moe_status_string(moe_status s);
 

@@ -19,6 +19,7 @@ LIB_PATH = os.path.join(_HERE, "libmoe.so")
 MOE_OK, MOE_ERR_INVALID_ARG, MOE_ERR_UNSUPPORTED, MOE_ERR_WORKSPACE, MOE_ERR_DEVICE = range(5)
 MOE_SCORE_SOFTMAX, MOE_SCORE_SIGMOID = 0, 1
 MOE_W_FP8_E4M3_B128, MOE_W_BF16, MOE_W_MXFP4_G32 = 0, 1, 2
+MOE_ROUTER_W_BF16, MOE_ROUTER_W_F32 = 0, 1
 SCORE_FN = {"softmax": MOE_SCORE_SOFTMAX, "sigmoid": MOE_SCORE_SIGMOID}
 
 EXPORTS = ("moe_route", "moe_permute_workspace_size", "moe_permute", "moe_expert_gate_up", "moe_expert_down",
@@ -26,7 +27,8 @@ EXPORTS = ("moe_route", "moe_permute_workspace_size", "moe_permute", "moe_expert
            "moe_expert_ffn_workspace_size", "moe_expert_ffn", "moe_combine", "moe_quantize_act",
            "moe_expert_gate_up_a8", "moe_expert_down_a8", "moe_expert_ffn_a8_workspace_size",
            "moe_expert_ffn_a8", "moe_combine_partial", "moe_route_permute",
-           "moe_permute_noalloc", "moe_status_string")
+           "moe_permute_noalloc", "moe_rmsnorm_quantize_act", "moe_router_scores_workspace_size",
+           "moe_router_scores", "moe_status_string")
 
 
 class MoeError(RuntimeError):
@@ -75,6 +77,10 @@ def lib():
         L.moe_expert_ffn_a8_workspace_size.argtypes = [i32, i32, W,
                                                        ctypes.POINTER(ctypes.c_size_t)]
         L.moe_expert_ffn_a8.argtypes = [P, i32, i32, P, P, W, P, P, ctypes.c_size_t, P]
+        L.moe_rmsnorm_quantize_act.argtypes = [P, P, P, i32, i32, ctypes.c_float, P, P, P, P, i32, P]
+        L.moe_router_scores_workspace_size.argtypes = [i32, i32, i32,
+                                                       ctypes.POINTER(ctypes.c_size_t)]
+        L.moe_router_scores.argtypes = [P, i32, i32, P, i32, i32, P, P, ctypes.c_size_t, P]
         for name in EXPORTS[:-1]:
             getattr(L, name).restype = st
         L.moe_status_string.argtypes = [st]
@@ -342,6 +348,114 @@ def moe_expert_ffn_a8(x, k: int, perm, offsets, w: MoeExpertWeights, y=None, ws=
         _p(x), T, k, _p(perm), _p(offsets), ctypes.byref(w), _p(y), _p(ws), ws.numel(),
         _s(stream)))
     return y, ws
+
+
+def _want(call, device, **tensors):
+    """Checks what a call takes of its tensors: name=(tensor or None, dtype, shape).  Raw pointers
+    are passed on, so a wrong layout would be read as another one."""
+    for name, (t, dtype, shape) in tensors.items():
+        if t is None:
+            continue
+        if t.dtype != dtype or t.shape != shape or not t.is_contiguous() or t.device != device:
+            raise ValueError(f"{call}: {name} must be a contiguous {dtype} tensor of shape "
+                             f"{tuple(shape)} on {device}, not {t.dtype} {tuple(t.shape)} with strides "
+                             f"{t.stride()} on {t.device}")
+
+
+class _On:
+    """The device and stream of one call: torch's current stream of the tensors' device (also when
+    another device is current), or the caller's `stream`.  Buffers that a call allocates itself
+    belong to that stream."""
+
+    def __init__(self, call, device, stream):
+        if device.type != "cuda":
+            raise ValueError(f"{call}: the tensors must be on a GPU, not on {device}")
+        if stream is None:
+            stream = torch.cuda.current_stream(device)
+            self.other = None
+        elif stream.device != device:
+            raise ValueError(f"{call}: the stream is of {stream.device}, the tensors are on {device}")
+        else:
+            self.other = stream
+        self.device, self.stream = device, ctypes.c_void_p(stream.cuda_stream)
+        self.current = device.index == torch.cuda.current_device()
+
+    def empty(self, shape, dtype):
+        if self.other is None:
+            return torch.empty(shape, dtype=dtype, device=self.device)
+        with torch.cuda.stream(self.other):
+            return torch.empty(shape, dtype=dtype, device=self.device)
+
+    def run(self, call, *args):
+        if self.current:
+            _check(call, getattr(lib(), call)(*args, self.stream))
+        else:
+            with torch.cuda.device(self.device):
+                _check(call, getattr(lib(), call)(*args, self.stream))
+
+
+def moe_rmsnorm_quantize_act(x, weight, residual=None, eps: float = 1e-6, normed=True,
+                             quantized=True, sum_out=None, y=None, codes=None, exps=None,
+                             pitch=None, stream=None):
+    """RMS norm of bf16 bits x [rows, K] (+ residual, added first) with the bf16 bits `weight` [K].
+    Returns (sum, y, codes, exps): the stored sum (None without a residual), the normalised rows
+    (None unless `normed`) and their FP8 codes and block exponents as moe_quantize_act's (None unless
+    `quantized`).  sum_out may be x or residual: the residual stream updated in place."""
+    call = "moe_rmsnorm_quantize_act"
+    if x.dim() != 2:
+        raise ValueError(f"{call}: x must have two dimensions")
+    on, (rows, K) = _On(call, x.device, stream), x.shape
+    if quantized:
+        pitch = exps.shape[1] if exps is not None else exp_pitch(K) if pitch is None else pitch
+    else:
+        codes = exps = None
+        pitch = 0
+    if not normed:
+        y = None
+    if residual is None and sum_out is not None:
+        raise ValueError(f"{call}: sum_out needs a residual")
+    shape, b16 = x.shape, torch.int16
+    _want(call, x.device, x=(x, b16, shape), weight=(weight, b16, (K,)),
+          residual=(residual, b16, shape), sum_out=(sum_out, b16, shape), y=(y, b16, shape),
+          codes=(codes, torch.uint8, shape), exps=(exps, torch.int8, (rows, pitch)))
+    if residual is not None and sum_out is None:
+        sum_out = on.empty(shape, b16)
+    if normed and y is None:
+        y = on.empty(shape, b16)
+    if quantized and codes is None:
+        codes = on.empty(shape, torch.uint8)
+    if quantized and exps is None:
+        exps = on.empty((rows, pitch), torch.int8)
+    on.run(call, _p(x), _p(residual), _p(weight), rows, K, eps, _p(sum_out), _p(y), _p(codes),
+           _p(exps), pitch)
+    return sum_out, y, codes, exps
+
+
+def moe_router_scores_workspace_size(T: int, H: int, E: int) -> int:
+    n = ctypes.c_size_t(0)
+    _check("moe_router_scores_workspace_size",
+           lib().moe_router_scores_workspace_size(T, H, E, ctypes.byref(n)))
+    return n.value
+
+
+def moe_router_scores(x, w, scores=None, ws=None, stream=None):
+    """Router scores fp32 [T, E] of bf16 bits x [T, H] with w [E, H] (bf16 bits, torch.int16, or
+    torch.float32).  `ws` (uint8 device tensor) is the call's workspace; None allocates one."""
+    call = "moe_router_scores"
+    if x.dim() != 2 or w.dim() != 2 or w.dtype not in (torch.int16, torch.float32):
+        raise ValueError(f"{call}: x [T, H] and w [E, H] (torch.int16 or torch.float32) are wanted")
+    on, (T, H), E = _On(call, x.device, stream), x.shape, w.shape[0]
+    _want(call, x.device, x=(x, torch.int16, x.shape), w=(w, w.dtype, (E, H)),
+          scores=(scores, torch.float32, (T, E)),
+          ws=(ws, torch.uint8, None if ws is None else (ws.numel(),)))
+    if scores is None:
+        scores = on.empty((T, E), torch.float32)
+    if ws is None and T > 16:
+        need = moe_router_scores_workspace_size(T, H, E)
+        ws = on.empty((need,), torch.uint8) if need else None
+    on.run(call, _p(x), T, H, _p(w), MOE_ROUTER_W_F32 if w.dtype == torch.float32 else MOE_ROUTER_W_BF16,
+           E, _p(scores), _p(ws), 0 if ws is None else ws.numel())
+    return scores
 
 
 def _permute_ws(T, k, E, device):

@@ -69,6 +69,16 @@ __device__ __forceinline__ float e8m0_to_f32(uint32_t s) {
     return __uint_as_float(s == 0 ? 0x00400000u : s == 255 ? 0x7fc00000u : s << 23);
 }
 
+// Exponent e of the power-of-two scale of a 128-block of FP8 activations with largest magnitude
+// amax: the smallest integer with amax <= 448 * 2^e, clamped to [-127, 127], 0 for a block of zeros.
+__device__ __forceinline__ int act_scale_exp(float amax) {
+    if (!(amax > 0.0f)) return 0;
+    int e2;
+    const float m = frexpf(amax, &e2);  // amax = m 2^e2, m in [0.5, 1)
+    int e = (m <= 0.875f) ? e2 - 9 : e2 - 8;
+    return min(127, max(-127, e));
+}
+
 __device__ __forceinline__ bf16x8 as_bf16x8(u32x4 v) { return __builtin_bit_cast(bf16x8, v); }
 
 // ------------------------------------------------------------------ wave primitives

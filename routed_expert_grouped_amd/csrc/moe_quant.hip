@@ -14,15 +14,6 @@
 
 namespace moe {
 
-// exponent e of the block scale for largest magnitude amax (see the file comment)
-__device__ __forceinline__ int act_scale_exp(float amax) {
-    if (!(amax > 0.0f)) return 0;
-    int e2;
-    const float m = frexpf(amax, &e2);  // amax = m 2^e2, m in [0.5, 1)
-    int e = (m <= 0.875f) ? e2 - 9 : e2 - 8;
-    return min(127, max(-127, e));
-}
-
 // One row of 16 lanes per (row, 128-block), four blocks a wave: lane l of the row holds values
 // 8l .. 8l + 7 (one 16-byte load), the block maximum is taken over the row with DPP row
 // operations (no cross-row traffic), and every lane converts its own eight values.  Writes any
