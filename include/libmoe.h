@@ -373,6 +373,36 @@ moe_status moe_router_scores(const uint16_t* x, int32_t T, int32_t H, const void
                              int32_t w_dtype, int32_t E, float* scores, void* ws, size_t ws_bytes,
                              void* stream);
 
+/* The whole layer for a few tokens (decode of up to MOE_FEW_MAX_TOKENS sequences) in two launches:
+ * route, gate/up, down, shared expert and combine [A2 4.1-4.2; OSDI "CPU fine-grained parallelism":
+ * gate and up before down, two synchronisations per layer]:
+ *     ids, w = moe_route(scores);  h_te = SiLU(Wg_e x_t) * (Wu_e x_t)
+ *     out[t] = bf16_rne( S_t + sum_j w_tj Wd_e h_te ),  e = ids[t][j]; S_t the shared expert's
+ *              output (weight 1), 0 without one
+ * Nothing between x and out is rounded to bf16: w_tj h_te is kept to 16 significand bits and every
+ * sum in fp32, so the result is closer to the formula than the separate calls' (which round h and
+ * y to bf16).  Sums run over the touched experts in ascending order, in parts that depend on the
+ * sizes and the routing alone: equal inputs give equal bits.  Each touched expert's weights are
+ * read once; a token's output depends on its own row and on the weights of its own experts.
+ *   scores : fp32 [T][E], finite, E = w->n_groups.     x : bf16 [T][H].
+ *   shared : one expert (n_groups == 1, dtype, H and I as w) or NULL.
+ *   topk_ids, topk_w : int32 [T][k], fp32 [T][k] out, bit for bit moe_route's.
+ *   out    : bf16 [T][H] out.
+ *   ws     : device workspace of ws_bytes >= moe_layer_few_workspace_size bytes, 16-byte aligned;
+ *            contents on entry do not matter; not used by other work until the launches complete.
+ * All three weight formats.  Limits: T <= MOE_FEW_MAX_TOKENS and T * (H + 8) <= 57408 (x stays in
+ * LDS: every T at H <= 7168, T <= 3 at H = 16384); the others as for moe_route and the expert
+ * calls.  Errors: INVALID_ARG for null or unaligned pointers, T < 0, k outside [1, E], an unknown
+ * score_fn, a shared expert that does not match w, and as for the expert calls; UNSUPPORTED beyond
+ * the limits; WORKSPACE when ws is NULL or too small.  T == 0 enqueues nothing. */
+#define MOE_FEW_MAX_TOKENS 8
+moe_status moe_layer_few_workspace_size(int32_t T, int32_t k, const moe_expert_weights* w,
+                                        size_t* bytes);
+moe_status moe_layer_few(const float* scores, const uint16_t* x, int32_t T, int32_t k,
+                         int32_t score_fn, int32_t renorm, const moe_expert_weights* w,
+                         const moe_expert_weights* shared, int32_t* topk_ids, float* topk_w,
+                         uint16_t* out, void* ws, size_t ws_bytes, void* stream);
+
 /* Static, human-readable name of a status code. */
 const char* moe_status_string(moe_status s);
 

@@ -28,7 +28,8 @@ EXPORTS = ("moe_route", "moe_permute_workspace_size", "moe_permute", "moe_expert
            "moe_expert_gate_up_a8", "moe_expert_down_a8", "moe_expert_ffn_a8_workspace_size",
            "moe_expert_ffn_a8", "moe_combine_partial", "moe_route_permute",
            "moe_permute_noalloc", "moe_rmsnorm_quantize_act", "moe_router_scores_workspace_size",
-           "moe_router_scores", "moe_status_string")
+           "moe_router_scores", "moe_layer_few_workspace_size", "moe_layer_few",
+           "moe_status_string")
 
 
 class MoeError(RuntimeError):
@@ -81,6 +82,8 @@ def lib():
         L.moe_router_scores_workspace_size.argtypes = [i32, i32, i32,
                                                        ctypes.POINTER(ctypes.c_size_t)]
         L.moe_router_scores.argtypes = [P, i32, i32, P, i32, i32, P, P, ctypes.c_size_t, P]
+        L.moe_layer_few_workspace_size.argtypes = [i32, i32, W, ctypes.POINTER(ctypes.c_size_t)]
+        L.moe_layer_few.argtypes = [P, P, i32, i32, i32, i32, W, W, P, P, P, P, ctypes.c_size_t, P]
         for name in EXPORTS[:-1]:
             getattr(L, name).restype = st
         L.moe_status_string.argtypes = [st]
@@ -456,6 +459,46 @@ def moe_router_scores(x, w, scores=None, ws=None, stream=None):
     on.run(call, _p(x), T, H, _p(w), MOE_ROUTER_W_F32 if w.dtype == torch.float32 else MOE_ROUTER_W_BF16,
            E, _p(scores), _p(ws), 0 if ws is None else ws.numel())
     return scores
+
+
+FEW_MAX_TOKENS = 8  # MOE_FEW_MAX_TOKENS
+
+
+def moe_layer_few_workspace_size(T: int, k: int, w: MoeExpertWeights) -> int:
+    n = ctypes.c_size_t(0)
+    _check("moe_layer_few_workspace_size",
+           lib().moe_layer_few_workspace_size(T, k, ctypes.byref(w), ctypes.byref(n)))
+    return n.value
+
+
+def moe_layer_few(scores, x, k: int, w: MoeExpertWeights, shared=None, score_fn="sigmoid",
+                  renorm: int = 1, topk_ids=None, topk_w=None, out=None, work=None, stream=None):
+    """The whole layer for up to FEW_MAX_TOKENS tokens in two launches; returns out (bf16 bits
+    [T, H]), topk_ids and topk_w.  `shared` is the shared expert's MoeExpertWeights or None; `work`
+    (uint8 device tensor) is the call's workspace, None allocates one."""
+    call = "moe_layer_few"
+    if x.dim() != 2 or scores.dim() != 2:
+        raise ValueError(f"{call}: scores [T, E] and x [T, H] are wanted")
+    on, (T, H) = _On(call, x.device, stream), x.shape
+    if H != w.H:
+        raise ValueError(f"{call}: x has rows of {H}, the weights take {w.H}")
+    _want(call, x.device, scores=(scores, torch.float32, (T, w.n_groups)), x=(x, torch.int16, x.shape),
+          topk_ids=(topk_ids, torch.int32, (T, k)), topk_w=(topk_w, torch.float32, (T, k)),
+          out=(out, torch.int16, x.shape),
+          work=(work, torch.uint8, None if work is None else (work.numel(),)))
+    fn = SCORE_FN[score_fn] if isinstance(score_fn, str) else int(score_fn)
+    if topk_ids is None:
+        topk_ids = on.empty((T, k), torch.int32)
+    if topk_w is None:
+        topk_w = on.empty((T, k), torch.float32)
+    if out is None:
+        out = on.empty((T, H), torch.int16)
+    if work is None:
+        work = on.empty((moe_layer_few_workspace_size(T, k, w),), torch.uint8)
+    on.run(call, _p(scores), _p(x), T, k, fn, int(renorm), ctypes.byref(w),
+           None if shared is None else ctypes.byref(shared), _p(topk_ids), _p(topk_w), _p(out), _p(work),
+           work.numel())
+    return out, topk_ids, topk_w
 
 
 def _permute_ws(T, k, E, device):

@@ -1,0 +1,613 @@
+// moe_few.hip -- a whole MoE layer for up to eight tokens in two launches.
+//
+// Decode of a few sequences reads every touched expert's three matrices once and does next to no
+// arithmetic on them (2 to 16 flops a byte): the weights' bytes bound it, and around them the launches and
+// the steps between them.  The layer is two streaming kernels:
+//
+//   few_gate_up   every workgroup routes the tokens for itself (scores are a few KB), then streams gate and
+//                 up rows of the touched experts: h_te = SiLU(Wg_e x_t) * (Wu_e x_t), stored as w_te * h_te.
+//   few_down      out_t = S_t + sum_e Wd_e (w_te h_te): with the gate weights already in h, the combine is
+//                 the same sum as the projection's.  A workgroup owns a few columns of out and runs one
+//                 product whose contraction is all touched experts' I in a row; no y, no permutation.
+//
+// Matrix tile (16x16x32 bf16, weights expanded exactly as in moe_ffn.hip): row m is token m, for every
+// expert, so that the activations need no gather: in few_gate_up all eight tokens' rows are multiplied and
+// those not routed to the expert are not stored; in few_down a token's sum takes the experts that it
+// is routed to, by a select when the expert's blocks end (so that what a weight does to one token's sum
+// cannot reach another's).
+//
+// h keeps fp32's precision: w_te * h_te goes on as two bf16 values, hi + lo (16 significand bits), in rows
+// t and 8 + t of the tile that eight tokens leave half empty, at no matrix instruction more.
+//
+// Work split: 8-wave workgroups, every wave a part of K.  few_gate_up: one workgroup per CU, looping over
+// units of 8 h columns (8 gate + 8 up rows); each wave streams its K part of unit after unit through a
+// ring of register stages that never drains between units, and the waves' sums meet in LDS once a
+// unit.  x (all tokens) stays in LDS, so that the ring's loads are weights alone: loads complete in
+// order, and a load of x behind them would wait for all of them.  The shared expert's unit comes first: its
+// loads are in flight while the routing runs.  few_down: a wave takes an even share of all (expert,
+// 128-block) stages of the workgroup's columns, and the waves' sums meet once at the end.
+#include "libmoe.h"
+#include "moe_device.h"
+#include "moe_ffn.h"
+#include "moe_host.h"
+#include "moe_lds.h"
+#include "moe_route.h"
+
+#include <algorithm>
+#include <type_traits>
+
+namespace moe {
+
+constexpr int kFewT = MOE_FEW_MAX_TOKENS;
+constexpr int kFewWaves = 8;
+constexpr int kFewThreads = kFewWaves * kWave;
+constexpr int kFewCols = 8;          // h columns of a few_gate_up unit
+constexpr int kFewXBytes = 114816;   // LDS for x: 8 rows of 7168 bf16, padded by 16 bytes each
+constexpr int kFewList = kFewT * MOE_MAX_TOPK;  // most touched experts
+constexpr int kFewShared = 0xFFFF;   // the shared expert's id in the list
+constexpr size_t kFewHead = 2048;    // workspace: list (count, then id | token mask << 16), then h
+static_assert((kFewList + 2) * sizeof(int32_t) <= kFewHead, "the list fits the workspace's head");
+
+struct FewArgs {
+    const float* scores;
+    const uint16_t* x;
+    int T, E, k, H, I, score_fn, renorm;
+    const void *g, *u, *d;     // routed experts
+    const void *sg, *su, *sd;  // their scales
+    const void *xg, *xu, *xd;  // the shared expert (null: none)
+    const void *xsg, *xsu, *xsd;
+    int32_t* ids;
+    float* wts;
+    int32_t* list;
+    uint16_t* h;  // [list index][2 T][I]: hi rows 0..T-1, lo rows T..2T-1
+    uint16_t* out;
+};
+
+constexpr int kFewBF16 = 0, kFewFP8 = 1, kFewMX = 2;
+
+template <int kFmt>
+struct FewFmt {
+    static constexpr int kBPS = kFmt == kFewMX ? 2 : 1;                            // 128-blocks a stage
+    static constexpr int kBB = kFmt == kFewFP8 ? 128 : kFmt == kFewMX ? 64 : 256;  // bytes of a row per block
+    static constexpr int kRowB = kBB * kBPS;                                       // bytes of a row per stage
+    static constexpr int kLD = kRowB + 16;   // LDS row stride: conflict-free reads
+    static constexpr int kLPR = kRowB / 16;  // lanes per row in a load instruction
+    static constexpr int kRPI = 64 / kLPR;   // rows per load instruction
+    static constexpr int kIns = 16 / kRPI;   // load instructions per 16 rows
+    // ring stages: about 8 KB (16 rows) in flight a wave, 64 KB a CU
+    static constexpr int kRing = kFmt == kFewBF16 ? 3 : 4;
+    static size_t row_bytes(int K) { return kFmt == kFewFP8 ? K : kFmt == kFewMX ? K / 2 : 2 * (size_t)K; }
+};
+
+// One 16-row weight group's fragments of block b from the wave's LDS rows, times the 16 activation rows'
+// fragments xv: returns the block's sums (f: this lane's MX group scale).
+template <int kFmt>
+__device__ __forceinline__ f32x4 few_block(const uint8_t* lds, int m, int kq, int b, const bf16x8* xv, float f) {
+    using F = FewFmt<kFmt>;
+    constexpr int kV = F::kBB / 64;
+    u32x4 rw[kV];
+#pragma unroll
+    for (int i = 0; i < kV; ++i) rw[i] = *(const u32x4*)&lds[m * F::kLD + b * F::kBB + kq * (F::kBB / 4) + i * 16];
+    f32x4 p = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t* u = (const uint32_t*)rw;
+        const bf16x8 wv = kFmt == kFewFP8 ? fp8x8_to_bf16x8(u[2 * i], u[2 * i + 1])
+                        : kFmt == kFewMX  ? fp4x8_to_bf16x8(u[i], f)
+                                          : as_bf16x8(rw[kFmt == kFewBF16 ? i : 0]);
+        p = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xv[i], wv, p, 0, 0, 0);
+    }
+    return p;
+}
+
+// A kernel argument as a global-memory pointer held in registers, and a choice between two of them by
+// value: left to itself, a choice between two arguments becomes a load from the chosen argument's address,
+// and waiting for that load would wait for the ring.
+typedef const __attribute__((address_space(1))) uint8_t* gbytes;
+template <typename V>
+using gvec = const __attribute__((address_space(1))) V*;
+
+__device__ __forceinline__ gbytes held(const void* p) {
+    uint64_t v = (uint64_t)p;
+    asm("" : "+s"(v));
+    return (gbytes)v;
+}
+template <typename P>
+__device__ __forceinline__ P pick(bool c, P a, P b) {
+    return c ? a : b;
+}
+
+// Waits for this wave's LDS operations, then the workgroup; loads in flight stay in flight.
+__device__ __forceinline__ void lds_barrier() {
+    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+}
+
+// f of slots 0 .. D - 1
+template <int D, int d = 0, typename F>
+__device__ __forceinline__ void each_slot(F&& f) {
+    f(std::integral_constant<int, d>{});
+    if constexpr (d + 1 < D) each_slot<D, d + 1>(f);
+}
+
+// n stages through a ring of D slots.  The loop goes round whole and has one exit, so that the compiler
+// sees every slot's loads behind the others' and its waits leave those in flight; the last n % D
+// stages follow it.
+template <int D, typename F>
+__device__ __forceinline__ void ring_loop(int n, F&& slot) {
+    int i = 0;
+    for (; i + D <= n; i += D) each_slot<D>(slot);
+    each_slot<D - 1>([&](auto tag) {
+        if (i + decltype(tag)::value < n) slot(tag);
+    });
+}
+
+template <int kFmt>
+__global__ __launch_bounds__(kFewThreads) void few_gate_up_kernel(FewArgs a) {
+    using F = FewFmt<kFmt>;
+    constexpr int D = F::kRing;
+    __shared__ __attribute__((aligned(16))) uint8_t sX[kFewXBytes];
+    __shared__ __attribute__((aligned(16))) uint8_t sW[kFewWaves][16 * F::kLD];
+    __shared__ f32x4 red[2][kFewWaves][32];
+    __shared__ int32_t sids[kFewList];
+    __shared__ float swts[kFewList];
+    __shared__ uint32_t bits[MOE_MAX_EXPERTS / 32];
+    __shared__ int32_t list[kFewList];
+    __shared__ int32_t count;
+
+    const int tid = (int)threadIdx.x, lane = lane_id(), wave = uniform(tid >> 6);
+    const int m = lane & 15, kq = lane >> 4;
+    const int T = a.T, H = a.H, I = a.I, k = a.k;
+    const gbytes Wg = held(a.g), Wu = held(a.u), Xg = held(a.xg), Xu = held(a.xu);
+    const gbytes Sg = held(a.sg), Su = held(a.su), XSg = held(a.xsg), XSu = held(a.xsu);
+    const int grid = (int)gridDim.x;
+    const bool shared = a.xg != nullptr;
+    const int tiles = I / kFewCols;
+    const int kb_all = H / 128, st_all = (kb_all + F::kBPS - 1) / F::kBPS;
+    const int st0 = st_all * wave / kFewWaves, ns = st_all * (wave + 1) / kFewWaves - st0;
+    const size_t row_bytes = kFmt == kFewFP8 ? (size_t)H : kFmt == kFewMX ? (size_t)H / 2 : (size_t)H * 2;
+    const int lrow = lane / F::kLPR, lchunk = lane % F::kLPR;
+    uint8_t* lds = sW[wave];
+
+    // ---- the ring of weight stages
+    u32x4 bw[D][F::kIns];
+    float sc[D];             // FP8: the scale of this lane's column (gate for columns 0..7, up for 8..15)
+    uint32_t mx[D][2];       // MXFP4: the scale bytes of this lane's row, two blocks
+    int iu = (int)blockIdx.x, ib = 0;  // issue cursor: unit, stage of this wave
+    int n_units = shared ? tiles : 0;  // (of the shared expert, until the routing is known)
+    gbytes gp{}, up{};  // this lane's first byte of the unit's gate / up rows
+    gbytes sp{};        // its scales
+    auto unit_of = [&](int unit) {  // pointers of a unit
+        const int u = unit / tiles, n0 = (unit - u * tiles) * kFewCols;
+        const bool xg = shared && u == 0;
+        const int e = xg ? 0 : uniform(list[u - (shared ? 1 : 0)]);
+        const size_t at = ((size_t)e * I + n0 + lrow) * row_bytes + (size_t)st0 * F::kRowB + lchunk * 16;
+        gp = pick(xg, Xg, Wg) + at;
+        up = pick(xg, Xu, Wu) + at;
+        const gbytes s = pick(m < 8, pick(xg, XSg, Sg), pick(xg, XSu, Su));
+        if (kFmt == kFewFP8) sp = s + 4 * (((size_t)e * (I / 128) + n0 / 128) * kb_all + st0);
+        if (kFmt == kFewMX) sp = s + ((size_t)e * I + n0 + (m & 7)) * (H / 32);
+    };
+    // loads of the cursor's stage into slot d, then one step of the cursor; past the last unit the last
+    // stage is loaded again (into slots that are not used), so that the loop's loads are unconditional
+    auto issue = [&](auto tag) {
+        constexpr int d = decltype(tag)::value;
+        size_t kofs = (size_t)ib * F::kRowB;
+        const int kb = (st0 + ib) * F::kBPS;
+        // a short last stage: the chunks of the missing block reload the first
+        if (F::kBPS > 1 && kb + 1 >= kb_all && lchunk >= F::kLPR / 2) kofs -= F::kRowB / 2;
+#pragma unroll
+        for (int i = 0; i < F::kIns; ++i) {
+            const size_t at = (size_t)(i % (F::kIns / 2)) * F::kRPI * row_bytes + kofs;
+            bw[d][i] = __builtin_nontemporal_load((gvec<u32x4>)((i < F::kIns / 2 ? gp : up) + at));
+        }
+        if (kFmt == kFewFP8) sc[d] = *(gvec<float>)(sp + 4 * ib);
+        if (kFmt == kFewMX) {
+            mx[d][0] = *(gvec<uint32_t>)(sp + 4 * kb);
+            mx[d][1] = *(gvec<uint32_t>)(sp + 4 * min(kb + 1, kb_all - 1));
+        }
+        if (ib + 1 < ns) {
+            ++ib;
+        } else if (iu + grid < n_units) {
+            iu += grid;
+            ib = 0;
+            unit_of(iu);
+        }
+    };
+
+    // the shared expert's first stages, before anything is known of the routing
+    const int pre = (shared && iu < n_units) ? min(D, ns) : 0;
+    if (pre > 0) {
+        unit_of(iu);
+        each_slot<D>([&](auto tag) {
+            if (decltype(tag)::value < pre) issue(tag);
+        });
+    }
+    // ---- x into LDS, rows padded by 16 bytes (row m starts 4 m banks on)
+    const int xrow = 2 * H + 16, chunks = H / 8;
+    for (int c = tid; c < T * chunks; c += kFewThreads) {
+        const int t = c / chunks, j = c - t * chunks;
+        *(u32x4*)&sX[t * xrow + 16 * j] = ((const u32x4*)(a.x + (size_t)t * H))[j];
+    }
+    // ---- routing: token t by wave t
+    if (tid < MOE_MAX_EXPERTS / 32) bits[tid] = 0u;
+    if (wave < T) {
+        const float* s = a.scores + (size_t)wave * a.E;
+        int32_t* ri = sids + wave * k;
+        float* rw = swts + wave * k;
+        if (a.E <= 64) route_token<1>(s, a.E, k, a.score_fn, a.renorm, ri, rw);
+        else if (a.E <= 128) route_token<2>(s, a.E, k, a.score_fn, a.renorm, ri, rw);
+        else if (a.E <= 256) route_token<4>(s, a.E, k, a.score_fn, a.renorm, ri, rw);
+        else if (a.E <= 512) route_token<8>(s, a.E, k, a.score_fn, a.renorm, ri, rw);
+        else route_token<16>(s, a.E, k, a.score_fn, a.renorm, ri, rw);
+    }
+    __syncthreads();
+    if (tid < T * k) atomicOr(&bits[sids[tid] >> 5], 1u << (sids[tid] & 31));
+    __syncthreads();
+    if (wave == 0) {  // the touched experts, ascending
+        const uint32_t w = lane < MOE_MAX_EXPERTS / 32 ? bits[lane] : 0u;
+        const int n = __popc(w), incl = wave_inclusive_scan(n);
+        int at = incl - n;
+        for (uint32_t r = w; r; r &= r - 1) list[at++] = 32 * lane + __ffs(r) - 1;
+        if (lane == kWave - 1) count = incl;
+    }
+    __syncthreads();
+    const int n_exp = uniform(count) + (shared ? 1 : 0);
+    n_units = n_exp * tiles;
+    if (blockIdx.x == 0) {  // for the second kernel and the caller
+        for (int i = tid; i < T * k; i += kFewThreads) {
+            a.ids[i] = sids[i];
+            a.wts[i] = swts[i];
+        }
+        for (int i = tid; i < n_exp; i += kFewThreads) {
+            const bool xg = shared && i == 0;
+            const int e = xg ? kFewShared : list[i - (shared ? 1 : 0)];
+            uint32_t mask = xg ? (1u << T) - 1 : 0u;
+            if (!xg)
+                for (int j = 0; j < T * k; ++j) mask |= sids[j] == e ? 1u << (j / k) : 0u;
+            a.list[1 + i] = (int32_t)((uint32_t)e | mask << 16);
+        }
+        if (tid == 0) a.list[0] = n_exp;
+    }
+    if ((int)blockIdx.x >= n_units) return;  // (whole workgroups)
+    if (ns > 0) {
+        // the issue cursor: at the shared unit's stage `pre`, or at the first unit's start
+        if (pre == 0) {
+            iu = (int)blockIdx.x;
+            ib = 0;
+            unit_of(iu);
+        } else if (pre == ns && iu == (int)blockIdx.x && iu + grid < n_units) {
+            // the whole shared unit is loaded, and its successor was not known yet
+            iu += grid;
+            ib = 0;
+            unit_of(iu);
+        }
+        each_slot<D>([&](auto tag) {
+            if (decltype(tag)::value >= pre) issue(tag);
+        });
+        // the conditional loads above end here, so that the loop's waits count its own loads only
+        __builtin_amdgcn_s_waitcnt(vmcnt_imm(0));
+    }
+
+    const int mrow = m < T ? m : 0;  // rows past the last token repeat token 0 (not stored)
+    f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+    auto compute = [&](auto tag, int st) {
+        constexpr int d = decltype(tag)::value;
+#pragma unroll
+        for (int i = 0; i < F::kIns; ++i)
+            *(u32x4*)&lds[(i * F::kRPI + lrow) * F::kLD + lchunk * 16] = bw[d][i];
+        __builtin_amdgcn_wave_barrier();  // (a wave's LDS operations complete in order)
+#pragma unroll
+        for (int b = 0; b < F::kBPS; ++b) {
+            const int kb = st * F::kBPS + b;
+            if (F::kBPS == 1 || kb < kb_all) {  // (the last stage may be one block)
+                bf16x8 xv[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    xv[i] = as_bf16x8(*(const u32x4*)&sX[mrow * xrow + kb * 256 + kq * 64 + i * 16]);
+                const float f = kFmt == kFewMX ? e8m0_to_f32((mx[d][b] >> (8 * kq)) & 255u) : 1.0f;
+                const f32x4 p = few_block<kFmt>(lds, m, kq, b, xv, f);
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                    acc[r] = kFmt == kFewFP8 ? fmaf(p[r], sc[d], acc[r]) : acc[r] + p[r];
+            }
+        }
+        __builtin_amdgcn_wave_barrier();
+        // the sums are taken here, not where they are next used: a scale that outlived its slot would be
+        // copied to another register every round, and that copy would wait for the whole ring
+        asm volatile("" : "+v"(acc));
+    };
+    int cu = (int)blockIdx.x, seq = 0;  // the unit being computed
+    // joins the waves' sums of the unit; wave seq % 8 then finishes its 8 columns
+    auto finish = [&]() {
+        if (lane < 32) red[seq & 1][wave][lane] = acc;  // tokens 0..7 are rows 0..7: lanes 0..31
+        acc = f32x4{0.f, 0.f, 0.f, 0.f};
+        lds_barrier();
+        if (wave == (seq & (kFewWaves - 1))) {
+            f32x4 v = red[seq & 1][0][lane & 31];
+#pragma unroll
+            for (int w = 1; w < kFewWaves; ++w) v += red[seq & 1][w][lane & 31];
+            const int u = cu / tiles, n0 = (cu - u * tiles) * kFewCols;
+            const bool xg = shared && u == 0;
+            const int e = xg ? 0 : list[u - (shared ? 1 : 0)];
+            float w[4];  // gate weights of tokens 4 kq + r (kq < 2), 0 for those not routed here
+            uint32_t mine = xg ? 15u : 0u;
+#pragma unroll
+            for (int r = 0; r < 4; ++r) w[r] = 1.0f;
+            if (!xg)
+                for (int j = 0; j < k; ++j)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        const int at = min(4 * kq + r, T - 1) * k + j;
+                        const bool hit = sids[at] == e;
+                        w[r] = hit ? swts[at] : w[r];
+                        mine |= hit ? 1u << r : 0u;
+                    }
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const float uv = __shfl(v[r], (lane & 48) | 8 | (lane & 7), kWave);
+                const int t = 4 * kq + r;
+                const float hv = w[r] * silu_mul(v[r], uv);
+                const uint16_t hi = f32_to_bf16(hv);
+                const float rest = hv - bf16_to_f32(hi);
+                if (m < 8 && t < T && (mine >> r & 1)) {
+                    const size_t at = ((size_t)u * 2 * T + t) * I + n0 + m;
+                    a.h[at] = hi;
+                    a.h[at + (size_t)T * I] = f32_to_bf16(isfinite(rest) ? rest : 0.0f);
+                }
+            }
+        }
+        ++seq;
+        cu += grid;
+    };
+    const int units = (n_units - (int)blockIdx.x + grid - 1) / grid;
+    if (ns == 0) {  // fewer stages than waves: this wave only takes part in the joins
+        for (int i = 0; i < units; ++i) finish();
+        return;
+    }
+    int cs = 0;
+    auto slot = [&](auto tag) {
+        compute(tag, st0 + cs);
+        __builtin_amdgcn_sched_barrier(0);
+        issue(tag);
+        __builtin_amdgcn_sched_barrier(0);
+        if (++cs == ns) {
+            cs = 0;
+            finish();
+        }
+    };
+    ring_loop<D>(units * ns, slot);
+}
+
+template <int kFmt, int kG>
+__global__ __launch_bounds__(kFewThreads) void few_down_kernel(FewArgs a) {
+    using F = FewFmt<kFmt>;
+    constexpr int D = kFmt == kFewMX ? 3 : F::kRing;  // (an MXFP4 stage holds two blocks of h)
+    __shared__ __attribute__((aligned(16))) uint8_t sW[kFewWaves][kG * 16 * F::kLD];
+    __shared__ f32x4 red[kFewWaves][kG][kWave];
+    __shared__ int32_t list[kFewList + 1];
+
+    const int tid = (int)threadIdx.x, lane = lane_id(), wave = uniform(tid >> 6);
+    const int m = lane & 15, kq = lane >> 4;
+    const int T = a.T, H = a.H, I = a.I;
+    const gbytes Wd = held(a.d), Xd = held(a.xd), Sd = held(a.sd), XSd = held(a.xsd), Hb = held(a.h);
+    const int n0 = (int)blockIdx.x * 16 * kG;
+    const int n_exp = uniform(a.list[0]);
+    for (int i = tid; i < n_exp; i += kFewThreads) list[i] = a.list[1 + i];
+    __syncthreads();
+    const int kb_all = I / 128, st_e = (kb_all + F::kBPS - 1) / F::kBPS;  // stages of an expert
+    const int S = n_exp * st_e;
+    const int q0 = (int)((int64_t)S * wave / kFewWaves), q1 = (int)((int64_t)S * (wave + 1) / kFewWaves);
+    const size_t row_bytes = kFmt == kFewFP8 ? (size_t)I : kFmt == kFewMX ? (size_t)I / 2 : (size_t)I * 2;
+    const int lrow = lane / F::kLPR, lchunk = lane % F::kLPR;
+    uint8_t* lds = sW[wave];
+
+    u32x4 bw[D][kG][F::kIns], hx[D][F::kBPS][4];
+    float sc[D];
+    uint32_t mx[D][kG][2];
+    int iu = 0, is = 0;  // issue cursor: list index, stage of the expert
+    gbytes wp{}, hp{}, sp{};  // this lane's weight, activation and scale bytes of the expert
+    auto expert_of = [&](int u) {
+        const uint32_t entry = (uint32_t)uniform(list[u]);
+        const int id = (int)(entry & 0xFFFF), mask = (int)(entry >> 16);
+        const bool xg = id == kFewShared;
+        const int e = xg ? 0 : id;
+        wp = pick(xg, Xd, Wd) + ((size_t)e * H + n0 + lrow) * row_bytes + lchunk * 16;
+        // rows of tokens that are not routed here hold nothing: such a lane reads another's row, and
+        // its sums are not taken
+        const int t = ((mask >> (m & 7)) & 1) ? (m & 7) : __ffs(mask) - 1;
+        hp = Hb + 2 * (((size_t)u * 2 * T + (m < 8 ? t : T + t)) * I + kq * 32);
+        const gbytes s = pick(xg, XSd, Sd);
+        if (kFmt == kFewFP8) sp = s + 4 * ((size_t)e * (H / 128) + n0 / 128) * kb_all;
+        if (kFmt == kFewMX) sp = s + ((size_t)e * H + n0 + m) * (I / 32);
+    };
+    int left = 0;  // stages not yet issued
+    auto issue = [&](auto tag) {
+        constexpr int d = decltype(tag)::value;
+        const int kb = is * F::kBPS;
+        size_t kofs = (size_t)is * F::kRowB;
+        if (F::kBPS > 1 && kb + 1 >= kb_all && lchunk >= F::kLPR / 2) kofs -= F::kRowB / 2;
+#pragma unroll
+        for (int g = 0; g < kG; ++g)
+#pragma unroll
+            for (int i = 0; i < F::kIns; ++i)
+                bw[d][g][i] = __builtin_nontemporal_load(
+                    (gvec<u32x4>)(wp + (size_t)(16 * g + i * F::kRPI) * row_bytes + kofs));
+#pragma unroll
+        for (int b = 0; b < F::kBPS; ++b)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) hx[d][b][i] = ((gvec<u32x4>)(hp + min(kb + b, kb_all - 1) * 256))[i];
+        if (kFmt == kFewFP8) sc[d] = *(gvec<float>)(sp + 4 * is);
+        if (kFmt == kFewMX) {
+#pragma unroll
+            for (int g = 0; g < kG; ++g) {
+                const gbytes row = sp + (size_t)16 * g * (I / 32);
+                mx[d][g][0] = *(gvec<uint32_t>)(row + 4 * kb);
+                mx[d][g][1] = *(gvec<uint32_t>)(row + 4 * min(kb + 1, kb_all - 1));
+            }
+        }
+        if (--left > 0) {  // (past the wave's share its last stage is loaded again, into unused slots)
+            if (++is == st_e) {
+                is = 0;
+                expert_of(++iu);
+            }
+        }
+    };
+    f32x4 acc[kG], pe[kG];  // sums of the experts done, and of the current one
+#pragma unroll
+    for (int g = 0; g < kG; ++g) acc[g] = pe[g] = f32x4{0.f, 0.f, 0.f, 0.f};
+    if (q0 < q1) {
+        iu = q0 / st_e;
+        is = q0 - iu * st_e;
+        int cu = iu, cs = is;  // the stage being computed
+        left = q1 - q0;
+        expert_of(iu);
+        each_slot<D>([&](auto tag) { issue(tag); });
+        auto compute = [&](auto tag) {
+            constexpr int d = decltype(tag)::value;
+#pragma unroll
+            for (int g = 0; g < kG; ++g)
+#pragma unroll
+                for (int i = 0; i < F::kIns; ++i)
+                    *(u32x4*)&lds[(16 * g + i * F::kRPI + lrow) * F::kLD + lchunk * 16] = bw[d][g][i];
+            __builtin_amdgcn_wave_barrier();
+#pragma unroll
+            for (int b = 0; b < F::kBPS; ++b) {
+                if (F::kBPS == 1 || cs * F::kBPS + b < kb_all) {
+                    bf16x8 xv[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) xv[i] = as_bf16x8(hx[d][b][i]);
+#pragma unroll
+                    for (int g = 0; g < kG; ++g) {
+                        const float f = kFmt == kFewMX ? e8m0_to_f32((mx[d][g][b] >> (8 * kq)) & 255u) : 1.0f;
+                        const f32x4 p = few_block<kFmt>(lds + 16 * g * F::kLD, m, kq, b, xv, f);
+#pragma unroll
+                        for (int r = 0; r < 4; ++r)
+                            pe[g][r] = kFmt == kFewFP8 ? fmaf(p[r], sc[d], pe[g][r]) : pe[g][r] + p[r];
+                    }
+                }
+            }
+            __builtin_amdgcn_wave_barrier();
+        };
+        auto flush = [&]() {  // the expert's sums, for the tokens routed to it (a wave's share may
+                              // begin or end inside an expert)
+            const int mask = (int)((uint32_t)uniform(list[cu]) >> 16);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const bool mine = (mask >> ((4 * kq + r) & 7)) & 1;
+#pragma unroll
+                for (int g = 0; g < kG; ++g) {
+                    acc[g][r] += mine ? pe[g][r] : 0.0f;
+                    pe[g][r] = 0.0f;
+                }
+            }
+        };
+        ring_loop<D>(q1 - q0, [&](auto tag) {
+            compute(tag);
+            __builtin_amdgcn_sched_barrier(0);
+            issue(tag);
+            __builtin_amdgcn_sched_barrier(0);
+            if (++cs == st_e) {
+                flush();
+                cs = 0;
+                ++cu;
+            }
+        });
+        if (cs != 0) flush();
+    }
+#pragma unroll
+    for (int g = 0; g < kG; ++g) red[wave][g][lane] = acc[g];
+    __syncthreads();
+    if (wave < kG) {  // wave g joins group g, in wave order, and adds the lo rows to the hi rows
+        f32x4 v = red[0][wave][lane];
+#pragma unroll
+        for (int w = 1; w < kFewWaves; ++w) v += red[w][wave][lane];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            const float lo = __shfl(v[r], lane | 32, kWave);
+            const int t = 4 * kq + r;
+            if (lane < 32 && t < T) a.out[(size_t)t * H + n0 + 16 * wave + m] = f32_to_bf16(v[r] + lo);
+        }
+    }
+}
+
+static moe_status check_few(int32_t T, int32_t k, const moe_expert_weights* w) {
+    if (T < 0 || k < 1) return MOE_ERR_INVALID_ARG;
+    const moe_status s = check_weights(w);
+    if (s != MOE_OK) return s;
+    if (k > w->n_groups) return MOE_ERR_INVALID_ARG;
+    if (k > MOE_MAX_TOPK || T > MOE_FEW_MAX_TOKENS) return MOE_ERR_UNSUPPORTED;
+    if (T * (2 * w->H + 16) > kFewXBytes) return MOE_ERR_UNSUPPORTED;
+    return MOE_OK;
+}
+
+static size_t few_ws(int T, int k, const moe_expert_weights* w) {
+    const size_t experts = std::min<int64_t>((int64_t)T * k, w->n_groups) + 1;  // and the shared one
+    return T == 0 ? 0 : kFewHead + experts * 2 * T * (size_t)w->I * sizeof(uint16_t);
+}
+
+template <int kFmt>
+static moe_status launch_few(const FewArgs& a, hipStream_t st) {
+    const int64_t units = ((int64_t)std::min(a.T * a.k, a.E) + 1) * (a.I / kFewCols);
+    few_gate_up_kernel<kFmt><<<dim3((unsigned)std::min<int64_t>(units, 256)), dim3(kFewThreads), 0, st>>>(a);
+    const moe_status s = launch_status();
+    if (s != MOE_OK) return s;
+    // 32 columns a workgroup where that leaves at least 7 of 8 CUs one, else 16
+    if (a.H / 32 >= 224) few_down_kernel<kFmt, 2><<<dim3((unsigned)(a.H / 32)), dim3(kFewThreads), 0, st>>>(a);
+    else few_down_kernel<kFmt, 1><<<dim3((unsigned)(a.H / 16)), dim3(kFewThreads), 0, st>>>(a);
+    return launch_status();
+}
+
+}  // namespace moe
+
+using namespace moe;
+
+extern "C" moe_status moe_layer_few_workspace_size(int32_t T, int32_t k, const moe_expert_weights* w,
+                                                   size_t* bytes) {
+    if (!bytes) return MOE_ERR_INVALID_ARG;
+    const moe_status s = check_few(T, k, w);
+    if (s != MOE_OK) return s;
+    *bytes = few_ws(T, k, w);
+    return MOE_OK;
+}
+
+extern "C" moe_status moe_layer_few(const float* scores, const uint16_t* x, int32_t T, int32_t k,
+                                    int32_t score_fn, int32_t renorm, const moe_expert_weights* w,
+                                    const moe_expert_weights* shared, int32_t* topk_ids, float* topk_w,
+                                    uint16_t* out, void* ws, size_t ws_bytes, void* stream) {
+    if (score_fn != MOE_SCORE_SOFTMAX && score_fn != MOE_SCORE_SIGMOID) return MOE_ERR_INVALID_ARG;
+    moe_status s = check_few(T, k, w);
+    if (s != MOE_OK) return s;
+    if (shared) {
+        if ((s = check_weights(shared)) != MOE_OK) return s;
+        if (shared->n_groups != 1 || shared->dtype != w->dtype || shared->H != w->H || shared->I != w->I)
+            return MOE_ERR_INVALID_ARG;
+    }
+    if (T == 0) return MOE_OK;
+    if (!scores || !x || !topk_ids || !topk_w || !out || !aligned16(scores) || !aligned16(x) ||
+        !aligned16(topk_ids) || !aligned16(topk_w) || !aligned16(out))
+        return MOE_ERR_INVALID_ARG;
+    if (!ws || ws_bytes < few_ws(T, k, w)) return MOE_ERR_WORKSPACE;
+    if (!aligned16(ws)) return MOE_ERR_INVALID_ARG;
+    FewArgs a{};
+    a.scores = scores;
+    a.x = x;
+    a.T = T, a.E = w->n_groups, a.k = k, a.H = w->H, a.I = w->I;
+    a.score_fn = score_fn, a.renorm = renorm;
+    a.g = w->w_gate, a.u = w->w_up, a.d = w->w_down;
+    a.sg = w->s_gate, a.su = w->s_up, a.sd = w->s_down;
+    if (shared) {
+        a.xg = shared->w_gate, a.xu = shared->w_up, a.xd = shared->w_down;
+        a.xsg = shared->s_gate, a.xsu = shared->s_up, a.xsd = shared->s_down;
+    }
+    a.ids = topk_ids;
+    a.wts = topk_w;
+    a.list = static_cast<int32_t*>(ws);
+    a.h = reinterpret_cast<uint16_t*>(static_cast<uint8_t*>(ws) + kFewHead);
+    a.out = out;
+    hipStream_t st = as_stream(stream);
+    switch (w->dtype) {
+        case MOE_W_BF16: return launch_few<kFewBF16>(a, st);
+        case MOE_W_FP8_E4M3_B128: return launch_few<kFewFP8>(a, st);
+        default: return launch_few<kFewMX>(a, st);
+    }
+}

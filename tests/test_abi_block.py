@@ -54,6 +54,42 @@ def test_router():
     assert size(0, 7168, 64, ctypes.byref(n)) == OK and n.value == 0
 
 
+def weights(dtype=0, n=4, H=256, I=128, ptr=FAKE, scales=True):
+    s = ptr.value if scales else None
+    return moe.MoeExpertWeights(dtype, n, H, I, ptr.value, ptr.value, ptr.value, s, s, s)
+
+
+def few(scores=FAKE, x=FAKE, T=4, k=2, fn=0, w=None, sh=None, ids=FAKE, tw=FAKE, out=FAKE, ws=FAKE, n=1 << 30):
+    w = weights() if w is None else w
+    return moe.lib().moe_layer_few(scores, x, T, k, fn, 1, ctypes.byref(w),
+                                   None if sh is None else ctypes.byref(sh), ids, tw, out, ws, n, None)
+
+
+def test_layer_few():
+    assert few(T=0) == OK and few(T=0, scores=None, x=None, ids=None, tw=None, out=None, ws=None) == OK
+    one = lambda **kw: weights(**(dict(n=1) | kw))  # noqa: E731
+    assert few(T=0, sh=one()) == OK
+    for bad in (dict(scores=None), dict(x=None), dict(ids=None), dict(tw=None), dict(out=None), dict(T=-1),
+                dict(k=0), dict(k=5), dict(fn=2), dict(scores=ODD), dict(x=ODD), dict(ids=ODD), dict(tw=ODD),
+                dict(out=ODD), dict(ws=ODD), dict(w=weights(dtype=3)), dict(w=weights(scales=False)),
+                dict(w=weights(ptr=ODD)), dict(sh=weights()), dict(sh=one(dtype=1)), dict(sh=one(H=128)),
+                dict(sh=one(I=256)), dict(sh=one(ptr=ODD))):
+        assert few(**bad) == INV, bad
+    for bad in (dict(T=9), dict(w=weights(H=200)), dict(w=weights(I=64)), dict(w=weights(n=1025)),
+                dict(w=weights(n=64), k=33), dict(w=weights(H=16384), T=4), dict(w=weights(H=7296), T=8)):
+        assert few(**bad) == UNS, bad
+    w = weights()
+    need = moe.moe_layer_few_workspace_size(4, 2, w)
+    assert need >= (4 + 1) * 2 * 4 * 128 * 2
+    assert few(ws=None) == WSP and few(n=need - 1) == WSP
+    assert moe.moe_layer_few_workspace_size(0, 2, w) == 0
+    n = ctypes.c_size_t(0)
+    size = moe.lib().moe_layer_few_workspace_size
+    assert size(4, 2, ctypes.byref(w), None) == INV and size(4, 2, None, ctypes.byref(n)) == INV
+    assert size(9, 2, ctypes.byref(w), ctypes.byref(n)) == UNS
+    assert size(3, 2, ctypes.byref(weights(H=16384)), ctypes.byref(n)) == OK
+
+
 def test_binding_needs_gpu_tensors():
     x, g = torch.zeros((4, 256), dtype=torch.int16), torch.zeros(256, dtype=torch.int16)
     with pytest.raises(ValueError):
