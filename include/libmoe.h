@@ -373,6 +373,24 @@ moe_status moe_router_scores(const uint16_t* x, int32_t T, int32_t H, const void
                              int32_t w_dtype, int32_t E, float* scores, void* ws, size_t ws_bytes,
                              void* stream);
 
+/* One dense projection on FP8 operands (a block's other projections, a dense FFN's matrices):
+ *     y[m][n] = bf16_rne( sum_b s_w[n/128][b] * 2^x_exps[m][b] * sum_{k in block b} x[m][k] w[n][k] )
+ * over the 128-blocks b of K [OSDI "native FP8 GEMV", Figures 9-10]: exact products, fp32 sums, a
+ * block's sum multiplied by its weight scale as it is added.
+ *   x_codes, x_exps : E4M3FN codes [M][K] and block exponents [M][exp_pitch] in [-127, 127], as
+ *                     moe_quantize_act and moe_rmsnorm_quantize_act write them; any exp_pitch >=
+ *                     K/128.
+ *   w   : E4M3FN codes [N][K] (nn.Linear layout).     s_w : fp32 [ceil(N/128)][K/128].
+ *   y   : bf16 [M][N] out.
+ * Any M (one row to many) and any N >= 1: the last scale row may cover fewer than 128 outputs.
+ * Errors: INVALID_ARG for M < 0, N < 1, K < 1, exp_pitch < K/128, null or unaligned pointers;
+ * UNSUPPORTED when K is not a multiple of 128, K > MOE_LINEAR_MAX_K, or the output has more than
+ * 2^22 tiles (of 16 x 16 values up to 16 rows, 128 x 128 at many).  M == 0 enqueues nothing. */
+#define MOE_LINEAR_MAX_K 65536
+moe_status moe_linear_a8(const uint8_t* x_codes, const int8_t* x_exps, int32_t exp_pitch, int32_t M,
+                         int32_t N, int32_t K, const uint8_t* w, const float* s_w, uint16_t* y,
+                         void* stream);
+
 /* The whole layer for a few tokens (decode of up to MOE_FEW_MAX_TOKENS sequences) in two launches:
  * route, gate/up, down, shared expert and combine [A2 4.1-4.2; OSDI "CPU fine-grained parallelism":
  * gate and up before down, two synchronisations per layer]:

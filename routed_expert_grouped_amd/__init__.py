@@ -29,7 +29,7 @@ EXPORTS = ("moe_route", "moe_permute_workspace_size", "moe_permute", "moe_expert
            "moe_expert_ffn_a8", "moe_combine_partial", "moe_route_permute",
            "moe_permute_noalloc", "moe_rmsnorm_quantize_act", "moe_router_scores_workspace_size",
            "moe_router_scores", "moe_layer_few_workspace_size", "moe_layer_few",
-           "moe_status_string")
+           "moe_linear_a8", "moe_status_string")
 
 
 class MoeError(RuntimeError):
@@ -84,6 +84,7 @@ def lib():
         L.moe_router_scores.argtypes = [P, i32, i32, P, i32, i32, P, P, ctypes.c_size_t, P]
         L.moe_layer_few_workspace_size.argtypes = [i32, i32, W, ctypes.POINTER(ctypes.c_size_t)]
         L.moe_layer_few.argtypes = [P, P, i32, i32, i32, i32, W, W, P, P, P, P, ctypes.c_size_t, P]
+        L.moe_linear_a8.argtypes = [P, P, i32, i32, i32, i32, P, P, P, P]
         for name in EXPORTS[:-1]:
             getattr(L, name).restype = st
         L.moe_status_string.argtypes = [st]
@@ -459,6 +460,22 @@ def moe_router_scores(x, w, scores=None, ws=None, stream=None):
     on.run(call, _p(x), T, H, _p(w), MOE_ROUTER_W_F32 if w.dtype == torch.float32 else MOE_ROUTER_W_BF16,
            E, _p(scores), _p(ws), 0 if ws is None else ws.numel())
     return scores
+
+
+def moe_linear_a8(codes, exps, w, s_w, y=None, stream=None):
+    """y = x W^T as bf16 bits [M, N]: x quantised by moe_quantize_act or moe_rmsnorm_quantize_act (codes
+    uint8 [M, K], exps int8 [M, pitch]), w uint8 [N, K] E4M3FN codes, s_w fp32 [ceil(N/128), K/128]."""
+    call = "moe_linear_a8"
+    if codes.dim() != 2 or w.dim() != 2 or exps.dim() != 2:
+        raise ValueError(f"{call}: codes [M, K], exps [M, pitch] and w [N, K] are wanted")
+    on, (M, K), N = _On(call, codes.device, stream), codes.shape, w.shape[0]
+    _want(call, codes.device, codes=(codes, torch.uint8, (M, K)), exps=(exps, torch.int8, (M, exps.shape[1])),
+          w=(w, torch.uint8, (N, K)), s_w=(s_w, torch.float32, (-(-N // 128), K // 128)),
+          y=(y, torch.int16, (M, N)))
+    if y is None:
+        y = on.empty((M, N), torch.int16)
+    on.run(call, _p(codes), _p(exps), exps.shape[1], M, N, K, _p(w), _p(s_w), _p(y))
+    return y
 
 
 FEW_MAX_TOKENS = 8  # MOE_FEW_MAX_TOKENS

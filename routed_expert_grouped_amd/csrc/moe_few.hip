@@ -31,10 +31,10 @@
 #include "moe_ffn.h"
 #include "moe_host.h"
 #include "moe_lds.h"
+#include "moe_ring.h"
 #include "moe_route.h"
 
 #include <algorithm>
-#include <type_traits>
 
 namespace moe {
 
@@ -100,45 +100,9 @@ __device__ __forceinline__ f32x4 few_block(const uint8_t* lds, int m, int kq, in
     return p;
 }
 
-// A kernel argument as a global-memory pointer held in registers, and a choice between two of them by
-// value: left to itself, a choice between two arguments becomes a load from the chosen argument's address,
-// and waiting for that load would wait for the ring.
-typedef const __attribute__((address_space(1))) uint8_t* gbytes;
-template <typename V>
-using gvec = const __attribute__((address_space(1))) V*;
-
-__device__ __forceinline__ gbytes held(const void* p) {
-    uint64_t v = (uint64_t)p;
-    asm("" : "+s"(v));
-    return (gbytes)v;
-}
-template <typename P>
-__device__ __forceinline__ P pick(bool c, P a, P b) {
-    return c ? a : b;
-}
-
 // Waits for this wave's LDS operations, then the workgroup; loads in flight stay in flight.
 __device__ __forceinline__ void lds_barrier() {
     asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
-}
-
-// f of slots 0 .. D - 1
-template <int D, int d = 0, typename F>
-__device__ __forceinline__ void each_slot(F&& f) {
-    f(std::integral_constant<int, d>{});
-    if constexpr (d + 1 < D) each_slot<D, d + 1>(f);
-}
-
-// n stages through a ring of D slots.  The loop goes round whole and has one exit, so that the compiler
-// sees every slot's loads behind the others' and its waits leave those in flight; the last n % D
-// stages follow it.
-template <int D, typename F>
-__device__ __forceinline__ void ring_loop(int n, F&& slot) {
-    int i = 0;
-    for (; i + D <= n; i += D) each_slot<D>(slot);
-    each_slot<D - 1>([&](auto tag) {
-        if (i + decltype(tag)::value < n) slot(tag);
-    });
 }
 
 template <int kFmt>
@@ -461,7 +425,11 @@ __global__ __launch_bounds__(kFewThreads) void few_down_kernel(FewArgs a) {
         int cu = iu, cs = is;  // the stage being computed
         left = q1 - q0;
         expert_of(iu);
-        each_slot<D>([&](auto tag) { issue(tag); });
+        // (in slot order, as the loop has them: the waits count on it)
+        each_slot<D>([&](auto tag) {
+            issue(tag);
+            __builtin_amdgcn_sched_barrier(0);
+        });
         auto compute = [&](auto tag) {
             constexpr int d = decltype(tag)::value;
 #pragma unroll

@@ -90,6 +90,19 @@ def test_layer_few():
     assert size(3, 2, ctypes.byref(weights(H=16384)), ctypes.byref(n)) == OK
 
 
+def linear(a=FAKE, e=FAKE, pitch=16, M=4, N=100, K=256, w=FAKE, s=FAKE, y=FAKE):
+    return moe.lib().moe_linear_a8(a, e, pitch, M, N, K, w, s, y, None)
+
+
+def test_linear():
+    assert linear(M=0) == OK and linear(M=0, a=None, e=None, w=None, s=None, y=None) == OK
+    for bad in (dict(a=None), dict(e=None), dict(w=None), dict(s=None), dict(y=None), dict(M=-1), dict(N=0),
+                dict(K=0), dict(pitch=1), dict(a=ODD), dict(e=ODD), dict(w=ODD), dict(s=ODD), dict(y=ODD)):
+        assert linear(**bad) == INV, bad
+    for bad in (dict(K=100), dict(K=65536 + 128, pitch=1024), dict(M=1 << 30, N=1 << 20)):
+        assert linear(**bad) == UNS, bad
+
+
 def test_binding_needs_gpu_tensors():
     x, g = torch.zeros((4, 256), dtype=torch.int16), torch.zeros(256, dtype=torch.int16)
     with pytest.raises(ValueError):
