@@ -41,7 +41,6 @@ namespace moe {
 constexpr int kFewT = MOE_FEW_MAX_TOKENS;
 constexpr int kFewWaves = 8;
 constexpr int kFewThreads = kFewWaves * kWave;
-constexpr int kFewCols = 8;          // h columns of a few_gate_up unit
 constexpr int kFewXBytes = 114816;   // LDS for x: 8 rows of 7168 bf16, padded by 16 bytes each
 constexpr int kFewList = kFewT * MOE_MAX_TOPK;  // most touched experts
 constexpr int kFewShared = 0xFFFF;   // the shared expert's id in the list
@@ -65,37 +64,50 @@ struct FewArgs {
 
 constexpr int kFewBF16 = 0, kFewFP8 = 1, kFewMX = 2;
 
+// A stage is 128 bytes (a cache line) of each of 16 weight rows.  A load instruction covers 8 rows; the
+// stage then goes through the wave's LDS rows once, to change from that layout to the matrix operand's.
 template <int kFmt>
 struct FewFmt {
-    static constexpr int kBPS = kFmt == kFewMX ? 2 : 1;                            // 128-blocks a stage
-    static constexpr int kBB = kFmt == kFewFP8 ? 128 : kFmt == kFewMX ? 64 : 256;  // bytes of a row per block
-    static constexpr int kRowB = kBB * kBPS;                                       // bytes of a row per stage
-    static constexpr int kLD = kRowB + 16;   // LDS row stride: conflict-free reads
-    static constexpr int kLPR = kRowB / 16;  // lanes per row in a load instruction
-    static constexpr int kRPI = 64 / kLPR;   // rows per load instruction
-    static constexpr int kIns = 16 / kRPI;   // load instructions per 16 rows
-    // ring stages: about 8 KB (16 rows) in flight a wave, 64 KB a CU
-    static constexpr int kRing = kFmt == kFewBF16 ? 3 : 4;
-    static size_t row_bytes(int K) { return kFmt == kFewFP8 ? K : kFmt == kFewMX ? K / 2 : 2 * (size_t)K; }
+    static constexpr int kSV = kFmt == kFewMX ? 256 : kFmt == kFewFP8 ? 128 : 64;  // values of a row per stage
+    static constexpr int kNM = kSV / 32;  // matrix instructions per stage and 16 rows
+    __device__ static size_t row_bytes(int K) { return kFmt == kFewMX ? K / 2 : kFmt == kFewFP8 ? K : 2 * (size_t)K; }
+    // The value (within the stage) of the first of the 8 values that lane quarter kq holds in
+    // instruction i: a quarter's values are consecutive weight bytes, a scale group in MXFP4
+    __device__ static int value(int i, int kq) {
+        return kFmt == kFewMX ? (i >> 2) * 128 + kq * 32 + (i & 3) * 8 : kq * (kSV / 4) + i * 8;
+    }
 };
+constexpr int kFewRing = 4;       // stages in flight a wave and 16 rows: 8 KB, 64 KB a CU
+constexpr int kFewLD = 128 + 16;  // LDS row stride of a stage: conflict-free reads
 
-// One 16-row weight group's fragments of block b from the wave's LDS rows, times the 16 activation rows'
-// fragments xv: returns the block's sums (f: this lane's MX group scale).
-template <int kFmt>
-__device__ __forceinline__ f32x4 few_block(const uint8_t* lds, int m, int kq, int b, const bf16x8* xv, float f) {
+// One stage of 16 weight rows through the wave's LDS rows, times the activation fragments x(i): the stage's
+// sums.  MXFP4: s0, s1 hold the scale bytes of the lane's row, a byte a quarter, for the stage's two
+// blocks; keep = 0 where the second block is past the end (its weights become zeros, its scale 1).
+template <int kFmt, typename X>
+__device__ __forceinline__ f32x4 few_stage(uint8_t* lds, const u32x4* w, int lane, uint32_t s0, uint32_t s1,
+                                           uint32_t keep, X&& x) {
     using F = FewFmt<kFmt>;
-    constexpr int kV = F::kBB / 64;
-    u32x4 rw[kV];
+    const int m = lane & 15, kq = lane >> 4;
 #pragma unroll
-    for (int i = 0; i < kV; ++i) rw[i] = *(const u32x4*)&lds[m * F::kLD + b * F::kBB + kq * (F::kBB / 4) + i * 16];
+    for (int i = 0; i < 2; ++i) *(u32x4*)&lds[(8 * i + (lane >> 3)) * kFewLD + (lane & 7) * 16] = w[i];
+    __builtin_amdgcn_wave_barrier();  // (a wave's LDS operations complete in order)
     f32x4 p = {0.f, 0.f, 0.f, 0.f};
+    const uint8_t* row = lds + m * kFewLD;
+    u32x4 v[2];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const uint32_t* u = (const uint32_t*)rw;
-        const bf16x8 wv = kFmt == kFewFP8 ? fp8x8_to_bf16x8(u[2 * i], u[2 * i + 1])
-                        : kFmt == kFewMX  ? fp4x8_to_bf16x8(u[i], f)
-                                          : as_bf16x8(rw[kFmt == kFewBF16 ? i : 0]);
-        p = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xv[i], wv, p, 0, 0, 0);
+    for (int i = 0; i < 2; ++i) v[i] = *(const u32x4*)&row[kFmt == kFewMX ? 64 * i + 16 * kq : 32 * kq + 16 * i];
+    __builtin_amdgcn_wave_barrier();
+    if (kFmt == kFewMX) {
+        v[1] &= keep;
+        s1 = keep ? s1 : 0x7F7F7F7Fu;
+    }
+#pragma unroll
+    for (int i = 0; i < F::kNM; ++i) {
+        const uint32_t* u = (const uint32_t*)v;
+        const bf16x8 wv = kFmt == kFewFP8 ? fp8x8_to_bf16x8(u[2 * (i & 3)], u[2 * (i & 3) + 1])
+                        : kFmt == kFewMX  ? fp4x8_to_bf16x8(u[i], e8m0_to_f32(((i < 4 ? s0 : s1) >> (8 * kq)) & 255u))
+                                          : as_bf16x8(v[i & 1]);
+        p = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x(i), wv, p, 0, 0, 0);
     }
     return p;
 }
@@ -105,17 +117,20 @@ __device__ __forceinline__ void lds_barrier() {
     asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
 }
 
-template <int kFmt>
+// kG: 16-row groups (8 gate + 8 up rows) of a unit
+template <int kFmt, int kG>
 __global__ __launch_bounds__(kFewThreads) void few_gate_up_kernel(FewArgs a) {
     using F = FewFmt<kFmt>;
-    constexpr int D = F::kRing;
+    constexpr int D = kFewRing, kCols = 8 * kG;
     __shared__ __attribute__((aligned(16))) uint8_t sX[kFewXBytes];
-    __shared__ __attribute__((aligned(16))) uint8_t sW[kFewWaves][16 * F::kLD];
-    __shared__ f32x4 red[2][kFewWaves][32];
+    __shared__ __attribute__((aligned(16))) uint8_t sW[kFewWaves][16 * kFewLD];
+    __shared__ float red[2][kFewWaves][kG][32 * 4];
     __shared__ int32_t sids[kFewList];
     __shared__ float swts[kFewList];
     __shared__ uint32_t bits[MOE_MAX_EXPERTS / 32];
-    __shared__ int32_t list[kFewList];
+    __shared__ int32_t base[MOE_MAX_EXPERTS / 32];  // touched experts before the word's
+    __shared__ uint32_t list[kFewList];             // touched experts, ascending: id | token mask << 16
+    __shared__ float wt[kFewList][kFewT];           // their gate weights for each token
     __shared__ int32_t count;
 
     const int tid = (int)threadIdx.x, lane = lane_id(), wave = uniform(tid >> 6);
@@ -124,27 +139,27 @@ __global__ __launch_bounds__(kFewThreads) void few_gate_up_kernel(FewArgs a) {
     const gbytes Wg = held(a.g), Wu = held(a.u), Xg = held(a.xg), Xu = held(a.xu);
     const gbytes Sg = held(a.sg), Su = held(a.su), XSg = held(a.xsg), XSu = held(a.xsu);
     const int grid = (int)gridDim.x;
-    const bool shared = a.xg != nullptr;
-    const int tiles = I / kFewCols;
-    const int kb_all = H / 128, st_all = (kb_all + F::kBPS - 1) / F::kBPS;
+    const int sh = a.xg != nullptr ? 1 : 0;
+    const int tiles = I / kCols;
+    const int kb_all = H / 128, st_all = (H + F::kSV - 1) / F::kSV;
     const int st0 = st_all * wave / kFewWaves, ns = st_all * (wave + 1) / kFewWaves - st0;
-    const size_t row_bytes = kFmt == kFewFP8 ? (size_t)H : kFmt == kFewMX ? (size_t)H / 2 : (size_t)H * 2;
-    const int lrow = lane / F::kLPR, lchunk = lane % F::kLPR;
+    const size_t row_bytes = F::row_bytes(H);
+    const int lrow = lane >> 3, lchunk = lane & 7;
     uint8_t* lds = sW[wave];
 
     // ---- the ring of weight stages
-    u32x4 bw[D][F::kIns];
-    float sc[D];             // FP8: the scale of this lane's column (gate for columns 0..7, up for 8..15)
-    uint32_t mx[D][2];       // MXFP4: the scale bytes of this lane's row, two blocks
-    int iu = (int)blockIdx.x, ib = 0;  // issue cursor: unit, stage of this wave
-    int n_units = shared ? tiles : 0;  // (of the shared expert, until the routing is known)
-    gbytes gp{}, up{};  // this lane's first byte of the unit's gate / up rows
-    gbytes sp{};        // its scales
+    u32x4 bw[D][kG][2];
+    float sc[D];              // FP8: the scale of this lane's column (gate for columns 0..7, up for 8..15)
+    uint32_t mx[D][kG][2];    // MXFP4: the scale bytes of this lane's row, two blocks
+    int iu = (int)blockIdx.x, ib = 0;   // issue cursor: unit, stage of this wave
+    int n_units = sh * tiles;  // (the shared expert's, until the routing is known)
+    gbytes gp{}, up{};         // this lane's first byte of the unit's gate / up rows
+    gbytes sp{};               // its scales
     auto unit_of = [&](int unit) {  // pointers of a unit
-        const int u = unit / tiles, n0 = (unit - u * tiles) * kFewCols;
-        const bool xg = shared && u == 0;
-        const int e = xg ? 0 : uniform(list[u - (shared ? 1 : 0)]);
-        const size_t at = ((size_t)e * I + n0 + lrow) * row_bytes + (size_t)st0 * F::kRowB + lchunk * 16;
+        const int u = unit / tiles, n0 = (unit - u * tiles) * kCols;
+        const bool xg = u < sh;
+        const int e = xg ? 0 : uniform((int)(list[u - sh] & 0xFFFFu));
+        const size_t at = ((size_t)e * I + n0 + lrow) * row_bytes + (size_t)st0 * 128 + lchunk * 16;
         gp = pick(xg, Xg, Wg) + at;
         up = pick(xg, Xu, Wu) + at;
         const gbytes s = pick(m < 8, pick(xg, XSg, Sg), pick(xg, XSu, Su));
@@ -155,19 +170,24 @@ __global__ __launch_bounds__(kFewThreads) void few_gate_up_kernel(FewArgs a) {
     // stage is loaded again (into slots that are not used), so that the loop's loads are unconditional
     auto issue = [&](auto tag) {
         constexpr int d = decltype(tag)::value;
-        size_t kofs = (size_t)ib * F::kRowB;
-        const int kb = (st0 + ib) * F::kBPS;
-        // a short last stage: the chunks of the missing block reload the first
-        if (F::kBPS > 1 && kb + 1 >= kb_all && lchunk >= F::kLPR / 2) kofs -= F::kRowB / 2;
+        size_t kofs = (size_t)ib * 128;
+        const int kb = 2 * (st0 + ib);  // MXFP4
+        // a short last MXFP4 stage: the chunks of the missing block reload the first
+        if (kFmt == kFewMX && kb + 1 >= kb_all && lchunk >= 4) kofs -= 64;
 #pragma unroll
-        for (int i = 0; i < F::kIns; ++i) {
-            const size_t at = (size_t)(i % (F::kIns / 2)) * F::kRPI * row_bytes + kofs;
-            bw[d][i] = __builtin_nontemporal_load((gvec<u32x4>)((i < F::kIns / 2 ? gp : up) + at));
+        for (int g = 0; g < kG; ++g) {
+            const size_t at = (size_t)8 * g * row_bytes + kofs;
+            bw[d][g][0] = __builtin_nontemporal_load((gvec<u32x4>)(gp + at));
+            bw[d][g][1] = __builtin_nontemporal_load((gvec<u32x4>)(up + at));
         }
         if (kFmt == kFewFP8) sc[d] = *(gvec<float>)(sp + 4 * ib);
         if (kFmt == kFewMX) {
-            mx[d][0] = *(gvec<uint32_t>)(sp + 4 * kb);
-            mx[d][1] = *(gvec<uint32_t>)(sp + 4 * min(kb + 1, kb_all - 1));
+#pragma unroll
+            for (int g = 0; g < kG; ++g) {
+                const gbytes row = sp + (size_t)8 * g * (H / 32);
+                mx[d][g][0] = *(gvec<uint32_t>)(row + 4 * kb);
+                mx[d][g][1] = *(gvec<uint32_t>)(row + 4 * min(kb + 1, kb_all - 1));
+            }
         }
         if (ib + 1 < ns) {
             ++ib;
@@ -179,21 +199,23 @@ __global__ __launch_bounds__(kFewThreads) void few_gate_up_kernel(FewArgs a) {
     };
 
     // the shared expert's first stages, before anything is known of the routing
-    const int pre = (shared && iu < n_units) ? min(D, ns) : 0;
+    const int pre = iu < n_units ? min(D, ns) : 0;
     if (pre > 0) {
         unit_of(iu);
         each_slot<D>([&](auto tag) {
             if (decltype(tag)::value < pre) issue(tag);
         });
     }
-    // ---- x into LDS, rows padded by 16 bytes (row m starts 4 m banks on)
+    // ---- x into LDS, rows padded by 16 bytes of zeros (row m starts 4 m banks on)
     const int xrow = 2 * H + 16, chunks = H / 8;
+    if (tid < T) *(u32x4*)&sX[tid * xrow + 2 * H] = u32x4{0u, 0u, 0u, 0u};
     for (int c = tid; c < T * chunks; c += kFewThreads) {
         const int t = c / chunks, j = c - t * chunks;
         *(u32x4*)&sX[t * xrow + 16 * j] = ((const u32x4*)(a.x + (size_t)t * H))[j];
     }
     // ---- routing: token t by wave t
     if (tid < MOE_MAX_EXPERTS / 32) bits[tid] = 0u;
+    if (tid < kFewList) list[tid] = 0u;
     if (wave < T) {
         const float* s = a.scores + (size_t)wave * a.E;
         int32_t* ri = sids + wave * k;
@@ -207,29 +229,28 @@ __global__ __launch_bounds__(kFewThreads) void few_gate_up_kernel(FewArgs a) {
     __syncthreads();
     if (tid < T * k) atomicOr(&bits[sids[tid] >> 5], 1u << (sids[tid] & 31));
     __syncthreads();
-    if (wave == 0) {  // the touched experts, ascending
-        const uint32_t w = lane < MOE_MAX_EXPERTS / 32 ? bits[lane] : 0u;
-        const int n = __popc(w), incl = wave_inclusive_scan(n);
-        int at = incl - n;
-        for (uint32_t r = w; r; r &= r - 1) list[at++] = 32 * lane + __ffs(r) - 1;
+    if (wave == 0) {
+        const int n = __popc(lane < MOE_MAX_EXPERTS / 32 ? bits[lane] : 0u), incl = wave_inclusive_scan(n);
+        if (lane < MOE_MAX_EXPERTS / 32) base[lane] = incl - n;
         if (lane == kWave - 1) count = incl;
     }
     __syncthreads();
-    const int n_exp = uniform(count) + (shared ? 1 : 0);
+    if (tid < T * k) {
+        const int e = sids[tid], t = tid / k;
+        const int u = base[e >> 5] + __popc(bits[e >> 5] & ((1u << (e & 31)) - 1u));
+        atomicOr(&list[u], (uint32_t)e | 1u << (16 + t));
+        wt[u][t] = swts[tid];
+    }
+    __syncthreads();
+    const int n_exp = uniform(count) + sh;
     n_units = n_exp * tiles;
     if (blockIdx.x == 0) {  // for the second kernel and the caller
         for (int i = tid; i < T * k; i += kFewThreads) {
             a.ids[i] = sids[i];
             a.wts[i] = swts[i];
         }
-        for (int i = tid; i < n_exp; i += kFewThreads) {
-            const bool xg = shared && i == 0;
-            const int e = xg ? kFewShared : list[i - (shared ? 1 : 0)];
-            uint32_t mask = xg ? (1u << T) - 1 : 0u;
-            if (!xg)
-                for (int j = 0; j < T * k; ++j) mask |= sids[j] == e ? 1u << (j / k) : 0u;
-            a.list[1 + i] = (int32_t)((uint32_t)e | mask << 16);
-        }
+        for (int i = tid; i < n_exp; i += kFewThreads)
+            a.list[1 + i] = i < sh ? (int32_t)(kFewShared | ((1u << T) - 1) << 16) : (int32_t)list[i - sh];
         if (tid == 0) a.list[0] = n_exp;
     }
     if ((int)blockIdx.x >= n_units) return;  // (whole workgroups)
@@ -252,72 +273,61 @@ __global__ __launch_bounds__(kFewThreads) void few_gate_up_kernel(FewArgs a) {
         __builtin_amdgcn_s_waitcnt(vmcnt_imm(0));
     }
 
-    const int mrow = m < T ? m : 0;  // rows past the last token repeat token 0 (not stored)
-    f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+    const uint8_t* xm = sX + (m < T ? m : 0) * xrow;  // rows past the last token repeat token 0 (not stored)
+    f32x4 acc[kG];
+#pragma unroll
+    for (int g = 0; g < kG; ++g) acc[g] = f32x4{0.f, 0.f, 0.f, 0.f};
     auto compute = [&](auto tag, int st) {
         constexpr int d = decltype(tag)::value;
+        const bool half = kFmt == kFewMX && 2 * st + 1 >= kb_all;  // a last stage of one block
+        bf16x8 xv[F::kNM];
 #pragma unroll
-        for (int i = 0; i < F::kIns; ++i)
-            *(u32x4*)&lds[(i * F::kRPI + lrow) * F::kLD + lchunk * 16] = bw[d][i];
-        __builtin_amdgcn_wave_barrier();  // (a wave's LDS operations complete in order)
-#pragma unroll
-        for (int b = 0; b < F::kBPS; ++b) {
-            const int kb = st * F::kBPS + b;
-            if (F::kBPS == 1 || kb < kb_all) {  // (the last stage may be one block)
-                bf16x8 xv[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    xv[i] = as_bf16x8(*(const u32x4*)&sX[mrow * xrow + kb * 256 + kq * 64 + i * 16]);
-                const float f = kFmt == kFewMX ? e8m0_to_f32((mx[d][b] >> (8 * kq)) & 255u) : 1.0f;
-                const f32x4 p = few_block<kFmt>(lds, m, kq, b, xv, f);
-#pragma unroll
-                for (int r = 0; r < 4; ++r)
-                    acc[r] = kFmt == kFewFP8 ? fmaf(p[r], sc[d], acc[r]) : acc[r] + p[r];
-            }
+        for (int i = 0; i < F::kNM; ++i) {
+            int at = 2 * (st * F::kSV + F::value(i, kq));
+            if (kFmt == kFewMX && i >= 4) at = half ? 2 * H : at;  // (the row's padding: zeros)
+            xv[i] = as_bf16x8(*(const u32x4*)&xm[at]);
         }
-        __builtin_amdgcn_wave_barrier();
-        // the sums are taken here, not where they are next used: a scale that outlived its slot would be
-        // copied to another register every round, and that copy would wait for the whole ring
-        asm volatile("" : "+v"(acc));
+#pragma unroll
+        for (int g = 0; g < kG; ++g) {
+            const f32x4 p = few_stage<kFmt>(lds, bw[d][g], lane, mx[d][g][0], mx[d][g][1], half ? 0u : ~0u,
+                                            [&](int i) { return xv[i]; });
+#pragma unroll
+            for (int r = 0; r < 4; ++r) acc[g][r] = kFmt == kFewFP8 ? fmaf(p[r], sc[d], acc[g][r]) : acc[g][r] + p[r];
+            // the sums are taken here, not where they are next used: a scale that outlived its slot would
+            // be copied to another register every round, and that copy would wait for the whole ring
+            asm volatile("" : "+v"(acc[g]));
+        }
     };
     int cu = (int)blockIdx.x, seq = 0;  // the unit being computed
-    // joins the waves' sums of the unit; wave seq % 8 then finishes its 8 columns
+    // Joins the waves' sums of the unit; kG of the waves, in turn, then finish its columns: wave
+    // kG seq + g takes group g, lane 8 t + c token t's column c.
     auto finish = [&]() {
-        if (lane < 32) red[seq & 1][wave][lane] = acc;  // tokens 0..7 are rows 0..7: lanes 0..31
-        acc = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int g = 0; g < kG; ++g) {
+            if (lane < 32) *(f32x4*)&red[seq & 1][wave][g][4 * lane] = acc[g];  // rows 0..7: lanes 0..31
+            acc[g] = f32x4{0.f, 0.f, 0.f, 0.f};
+        }
         lds_barrier();
-        if (wave == (seq & (kFewWaves - 1))) {
-            f32x4 v = red[seq & 1][0][lane & 31];
+        const int g = (wave - kG * seq) & (kFewWaves - 1);
+        if (g < kG) {
+            const int t = lane >> 3, c = lane & 7;
+            // D layout: token t is value t % 4 of lanes 16 (t / 4) + column; gate column c, up column 8 + c
+            const int at = 64 * (t >> 2) + 4 * c + (t & 3);
+            float gv = 0.0f, uv = 0.0f;
 #pragma unroll
-            for (int w = 1; w < kFewWaves; ++w) v += red[seq & 1][w][lane & 31];
-            const int u = cu / tiles, n0 = (cu - u * tiles) * kFewCols;
-            const bool xg = shared && u == 0;
-            const int e = xg ? 0 : list[u - (shared ? 1 : 0)];
-            float w[4];  // gate weights of tokens 4 kq + r (kq < 2), 0 for those not routed here
-            uint32_t mine = xg ? 15u : 0u;
-#pragma unroll
-            for (int r = 0; r < 4; ++r) w[r] = 1.0f;
-            if (!xg)
-                for (int j = 0; j < k; ++j)
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) {
-                        const int at = min(4 * kq + r, T - 1) * k + j;
-                        const bool hit = sids[at] == e;
-                        w[r] = hit ? swts[at] : w[r];
-                        mine |= hit ? 1u << r : 0u;
-                    }
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const float uv = __shfl(v[r], (lane & 48) | 8 | (lane & 7), kWave);
-                const int t = 4 * kq + r;
-                const float hv = w[r] * silu_mul(v[r], uv);
+            for (int w = 0; w < kFewWaves; ++w) {
+                gv += red[seq & 1][w][g][at];
+                uv += red[seq & 1][w][g][at + 32];
+            }
+            const int u = cu / tiles, n0 = (cu - u * tiles) * kCols;
+            const uint32_t mask = u < sh ? (1u << T) - 1 : list[u - sh] >> 16;
+            const float hv = (u < sh ? 1.0f : wt[u - sh][t]) * silu_mul(gv, uv);
+            if (mask >> t & 1) {
                 const uint16_t hi = f32_to_bf16(hv);
                 const float rest = hv - bf16_to_f32(hi);
-                if (m < 8 && t < T && (mine >> r & 1)) {
-                    const size_t at = ((size_t)u * 2 * T + t) * I + n0 + m;
-                    a.h[at] = hi;
-                    a.h[at + (size_t)T * I] = f32_to_bf16(isfinite(rest) ? rest : 0.0f);
-                }
+                uint16_t* h = a.h + ((size_t)u * 2 * T + t) * I + n0 + 8 * g + c;
+                h[0] = hi;
+                h[(size_t)T * I] = f32_to_bf16(isfinite(rest) ? rest : 0.0f);
             }
         }
         ++seq;
@@ -329,7 +339,7 @@ __global__ __launch_bounds__(kFewThreads) void few_gate_up_kernel(FewArgs a) {
         return;
     }
     int cs = 0;
-    auto slot = [&](auto tag) {
+    ring_loop<D>(units * ns, [&](auto tag) {
         compute(tag, st0 + cs);
         __builtin_amdgcn_sched_barrier(0);
         issue(tag);
@@ -338,17 +348,17 @@ __global__ __launch_bounds__(kFewThreads) void few_gate_up_kernel(FewArgs a) {
             cs = 0;
             finish();
         }
-    };
-    ring_loop<D>(units * ns, slot);
+    });
 }
 
+// kG: 16-column groups of a workgroup
 template <int kFmt, int kG>
 __global__ __launch_bounds__(kFewThreads) void few_down_kernel(FewArgs a) {
     using F = FewFmt<kFmt>;
-    constexpr int D = kFmt == kFewMX ? 3 : F::kRing;  // (an MXFP4 stage holds two blocks of h)
-    __shared__ __attribute__((aligned(16))) uint8_t sW[kFewWaves][kG * 16 * F::kLD];
+    constexpr int D = kFmt == kFewMX ? 3 : kFewRing;  // (an MXFP4 stage holds two blocks of h)
+    __shared__ __attribute__((aligned(16))) uint8_t sW[kFewWaves][16 * kFewLD];
     __shared__ f32x4 red[kFewWaves][kG][kWave];
-    __shared__ int32_t list[kFewList + 1];
+    __shared__ uint32_t list[kFewList + 1];
 
     const int tid = (int)threadIdx.x, lane = lane_id(), wave = uniform(tid >> 6);
     const int m = lane & 15, kq = lane >> 4;
@@ -356,22 +366,22 @@ __global__ __launch_bounds__(kFewThreads) void few_down_kernel(FewArgs a) {
     const gbytes Wd = held(a.d), Xd = held(a.xd), Sd = held(a.sd), XSd = held(a.xsd), Hb = held(a.h);
     const int n0 = (int)blockIdx.x * 16 * kG;
     const int n_exp = uniform(a.list[0]);
-    for (int i = tid; i < n_exp; i += kFewThreads) list[i] = a.list[1 + i];
+    for (int i = tid; i < n_exp; i += kFewThreads) list[i] = (uint32_t)a.list[1 + i];
     __syncthreads();
-    const int kb_all = I / 128, st_e = (kb_all + F::kBPS - 1) / F::kBPS;  // stages of an expert
+    const int kb_all = I / 128, st_e = (I + F::kSV - 1) / F::kSV;  // stages of an expert
     const int S = n_exp * st_e;
     const int q0 = (int)((int64_t)S * wave / kFewWaves), q1 = (int)((int64_t)S * (wave + 1) / kFewWaves);
-    const size_t row_bytes = kFmt == kFewFP8 ? (size_t)I : kFmt == kFewMX ? (size_t)I / 2 : (size_t)I * 2;
-    const int lrow = lane / F::kLPR, lchunk = lane % F::kLPR;
+    const size_t row_bytes = F::row_bytes(I);
+    const int lrow = lane >> 3, lchunk = lane & 7;
     uint8_t* lds = sW[wave];
 
-    u32x4 bw[D][kG][F::kIns], hx[D][F::kBPS][4];
+    u32x4 bw[D][kG][2], hx[D][F::kNM];
     float sc[D];
     uint32_t mx[D][kG][2];
-    int iu = 0, is = 0;  // issue cursor: list index, stage of the expert
+    int iu = 0, is = 0;       // issue cursor: list index, stage of the expert
     gbytes wp{}, hp{}, sp{};  // this lane's weight, activation and scale bytes of the expert
     auto expert_of = [&](int u) {
-        const uint32_t entry = (uint32_t)uniform(list[u]);
+        const uint32_t entry = (uint32_t)uniform((int)list[u]);
         const int id = (int)(entry & 0xFFFF), mask = (int)(entry >> 16);
         const bool xg = id == kFewShared;
         const int e = xg ? 0 : id;
@@ -379,7 +389,7 @@ __global__ __launch_bounds__(kFewThreads) void few_down_kernel(FewArgs a) {
         // rows of tokens that are not routed here hold nothing: such a lane reads another's row, and
         // its sums are not taken
         const int t = ((mask >> (m & 7)) & 1) ? (m & 7) : __ffs(mask) - 1;
-        hp = Hb + 2 * (((size_t)u * 2 * T + (m < 8 ? t : T + t)) * I + kq * 32);
+        hp = Hb + 2 * ((size_t)u * 2 * T + (m < 8 ? t : T + t)) * I;
         const gbytes s = pick(xg, XSd, Sd);
         if (kFmt == kFewFP8) sp = s + 4 * ((size_t)e * (H / 128) + n0 / 128) * kb_all;
         if (kFmt == kFewMX) sp = s + ((size_t)e * H + n0 + m) * (I / 32);
@@ -387,19 +397,22 @@ __global__ __launch_bounds__(kFewThreads) void few_down_kernel(FewArgs a) {
     int left = 0;  // stages not yet issued
     auto issue = [&](auto tag) {
         constexpr int d = decltype(tag)::value;
-        const int kb = is * F::kBPS;
-        size_t kofs = (size_t)is * F::kRowB;
-        if (F::kBPS > 1 && kb + 1 >= kb_all && lchunk >= F::kLPR / 2) kofs -= F::kRowB / 2;
+        const int kb = 2 * is;  // MXFP4
+        size_t kofs = (size_t)is * 128;
+        const bool half = kFmt == kFewMX && kb + 1 >= kb_all;  // a last stage of one block
+        if (half && lchunk >= 4) kofs -= 64;
 #pragma unroll
         for (int g = 0; g < kG; ++g)
 #pragma unroll
-            for (int i = 0; i < F::kIns; ++i)
+            for (int i = 0; i < 2; ++i)
                 bw[d][g][i] = __builtin_nontemporal_load(
-                    (gvec<u32x4>)(wp + (size_t)(16 * g + i * F::kRPI) * row_bytes + kofs));
+                    (gvec<u32x4>)(wp + (size_t)(16 * g + 8 * i) * row_bytes + kofs));
 #pragma unroll
-        for (int b = 0; b < F::kBPS; ++b)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) hx[d][b][i] = ((gvec<u32x4>)(hp + min(kb + b, kb_all - 1) * 256))[i];
+        for (int i = 0; i < F::kNM; ++i) {
+            int v = is * F::kSV + F::value(i, kq);
+            if (half && i >= 4) v -= 128;
+            hx[d][i] = *(gvec<u32x4>)(hp + 2 * v);
+        }
         if (kFmt == kFewFP8) sc[d] = *(gvec<float>)(sp + 4 * is);
         if (kFmt == kFewMX) {
 #pragma unroll
@@ -432,33 +445,19 @@ __global__ __launch_bounds__(kFewThreads) void few_down_kernel(FewArgs a) {
         });
         auto compute = [&](auto tag) {
             constexpr int d = decltype(tag)::value;
+            const bool half = kFmt == kFewMX && 2 * cs + 1 >= kb_all;
 #pragma unroll
-            for (int g = 0; g < kG; ++g)
+            for (int g = 0; g < kG; ++g) {
+                const f32x4 p = few_stage<kFmt>(lds, bw[d][g], lane, mx[d][g][0], mx[d][g][1], half ? 0u : ~0u,
+                                                [&](int i) { return as_bf16x8(hx[d][i]); });
 #pragma unroll
-                for (int i = 0; i < F::kIns; ++i)
-                    *(u32x4*)&lds[(16 * g + i * F::kRPI + lrow) * F::kLD + lchunk * 16] = bw[d][g][i];
-            __builtin_amdgcn_wave_barrier();
-#pragma unroll
-            for (int b = 0; b < F::kBPS; ++b) {
-                if (F::kBPS == 1 || cs * F::kBPS + b < kb_all) {
-                    bf16x8 xv[4];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) xv[i] = as_bf16x8(hx[d][b][i]);
-#pragma unroll
-                    for (int g = 0; g < kG; ++g) {
-                        const float f = kFmt == kFewMX ? e8m0_to_f32((mx[d][g][b] >> (8 * kq)) & 255u) : 1.0f;
-                        const f32x4 p = few_block<kFmt>(lds + 16 * g * F::kLD, m, kq, b, xv, f);
-#pragma unroll
-                        for (int r = 0; r < 4; ++r)
-                            pe[g][r] = kFmt == kFewFP8 ? fmaf(p[r], sc[d], pe[g][r]) : pe[g][r] + p[r];
-                    }
-                }
+                for (int r = 0; r < 4; ++r) pe[g][r] = kFmt == kFewFP8 ? fmaf(p[r], sc[d], pe[g][r]) : pe[g][r] + p[r];
+                asm volatile("" : "+v"(pe[g]));
             }
-            __builtin_amdgcn_wave_barrier();
         };
         auto flush = [&]() {  // the expert's sums, for the tokens routed to it (a wave's share may
                               // begin or end inside an expert)
-            const int mask = (int)((uint32_t)uniform(list[cu]) >> 16);
+            const int mask = (int)((uint32_t)uniform((int)list[cu]) >> 16);
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
                 const bool mine = (mask >> ((4 * kq + r) & 7)) & 1;
@@ -515,8 +514,13 @@ static size_t few_ws(int T, int k, const moe_expert_weights* w) {
 
 template <int kFmt>
 static moe_status launch_few(const FewArgs& a, hipStream_t st) {
-    const int64_t units = ((int64_t)std::min(a.T * a.k, a.E) + 1) * (a.I / kFewCols);
-    few_gate_up_kernel<kFmt><<<dim3((unsigned)std::min<int64_t>(units, 256)), dim3(kFewThreads), 0, st>>>(a);
+    // units of 16 columns where there are many of them, of 8 where whole rounds of the workgroups matter
+    const int64_t experts = std::min(a.T * a.k, a.E) + 1;
+    const bool wide = experts * a.I >= 16 * 4096;
+    const int64_t units = experts * (a.I / (wide ? 16 : 8));
+    const dim3 grid((unsigned)std::min<int64_t>(units, 256)), block(kFewThreads);
+    if (wide) few_gate_up_kernel<kFmt, 2><<<grid, block, 0, st>>>(a);
+    else few_gate_up_kernel<kFmt, 1><<<grid, block, 0, st>>>(a);
     const moe_status s = launch_status();
     if (s != MOE_OK) return s;
     // 32 columns a workgroup where that leaves at least 7 of 8 CUs one, else 16
