@@ -80,36 +80,67 @@ struct FewFmt {
 constexpr int kFewRing = 4;       // stages in flight a wave and 16 rows: 8 KB, 64 KB a CU
 constexpr int kFewLD = 128 + 16;  // LDS row stride of a stage: conflict-free reads
 
-// One stage of 16 weight rows through the wave's LDS rows, times the activation fragments x(i): the stage's
-// sums.  MXFP4: s0, s1 hold the scale bytes of the lane's row, a byte a quarter, for the stage's two
-// blocks; keep = 0 where the second block is past the end (its weights become zeros, its scale 1).
-template <int kFmt, typename X>
-__device__ __forceinline__ f32x4 few_stage(uint8_t* lds, const u32x4* w, int lane, uint32_t s0, uint32_t s1,
-                                           uint32_t keep, X&& x) {
+// MXFP4 scales: the stage's 16 kG rows have 8 bytes each, far apart.  One load instruction takes them all,
+// lane 2 r + b the dword of row r's block b: two lanes a row, 32 accesses.  (With every lane loading the
+// dword of its own row and block, four quarters asking for the same one, the address unit took 64 cycles for
+// each of 2 kG instructions a stage, and bounded the kernel: 284 K of 415 K cycles at 8 tokens.)
+__device__ __forceinline__ int mx_row(int lane, int kG) { return (lane >> 1) & (16 * kG - 1); }
+
+// One stage of kG times 16 weight rows, times the activation fragments x(i): the stage's sums.  Each group
+// goes through the same LDS rows (a wave's LDS operations complete in order), all groups before the first
+// product; the products run in two chains a group, so that a wave has 2 kG independent ones in flight.
+// MXFP4: sv holds the stage's scale dwords (four scale bytes, one a quarter, per row and block) as
+// mx_row() says, row r's block b in lane 2 r + b; keep = 0 where the second block is past the end
+// (its weights become zeros, its scale 1).
+template <int kFmt, int kG, typename X>
+__device__ __forceinline__ void few_stage(uint8_t* lds, const u32x4 (*w)[2], int lane, uint32_t sv, uint32_t keep,
+                                          X&& x, f32x4* p) {
     using F = FewFmt<kFmt>;
     const int m = lane & 15, kq = lane >> 4;
-#pragma unroll
-    for (int i = 0; i < 2; ++i) *(u32x4*)&lds[(8 * i + (lane >> 3)) * kFewLD + (lane & 7) * 16] = w[i];
-    __builtin_amdgcn_wave_barrier();  // (a wave's LDS operations complete in order)
-    f32x4 p = {0.f, 0.f, 0.f, 0.f};
     const uint8_t* row = lds + m * kFewLD;
-    u32x4 v[2];
+    u32x4 v[kG][2];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) v[i] = *(const u32x4*)&row[kFmt == kFewMX ? 64 * i + 16 * kq : 32 * kq + 16 * i];
-    __builtin_amdgcn_wave_barrier();
+    for (int g = 0; g < kG; ++g) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) *(u32x4*)&lds[(8 * i + (lane >> 3)) * kFewLD + (lane & 7) * 16] = w[g][i];
+        __builtin_amdgcn_wave_barrier();
+#pragma unroll
+        for (int i = 0; i < 2; ++i) v[g][i] = *(const u32x4*)&row[kFmt == kFewMX ? 64 * i + 16 * kq : 32 * kq + 16 * i];
+        __builtin_amdgcn_wave_barrier();
+    }
+    float f[kG][2];
     if (kFmt == kFewMX) {
-        v[1] &= keep;
-        s1 = keep ? s1 : 0x7F7F7F7Fu;
-    }
 #pragma unroll
-    for (int i = 0; i < F::kNM; ++i) {
-        const uint32_t* u = (const uint32_t*)v;
-        const bf16x8 wv = kFmt == kFewFP8 ? fp8x8_to_bf16x8(u[2 * (i & 3)], u[2 * (i & 3) + 1])
-                        : kFmt == kFewMX  ? fp4x8_to_bf16x8(u[i], e8m0_to_f32(((i < 4 ? s0 : s1) >> (8 * kq)) & 255u))
-                                          : as_bf16x8(v[i & 1]);
-        p = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x(i), wv, p, 0, 0, 0);
+        for (int g = 0; g < kG; ++g) {
+            v[g][1] &= keep;
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+                const uint32_t w4 = (uint32_t)__builtin_amdgcn_ds_bpermute(4 * (2 * (16 * g + m) + b), (int)sv);
+                f[g][b] = e8m0_to_f32(((b == 0 || keep ? w4 : 0x7F7F7F7Fu) >> (8 * kq)) & 255u);
+            }
+        }
     }
-    return p;
+    constexpr int kHalf = F::kNM / 2;
+    f32x4 q[kG][2];
+#pragma unroll
+    for (int g = 0; g < kG; ++g) q[g][0] = q[g][1] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int j = 0; j < kHalf; ++j)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+            const int i = c * kHalf + j;
+            const bf16x8 xv = x(i);
+#pragma unroll
+            for (int g = 0; g < kG; ++g) {
+                const uint32_t* u = (const uint32_t*)v[g];
+                const bf16x8 wv = kFmt == kFewFP8 ? fp8x8_to_bf16x8(u[2 * (i & 3)], u[2 * (i & 3) + 1])
+                                : kFmt == kFewMX  ? fp4x8_to_bf16x8(u[i], f[g][i >> 2])
+                                                  : as_bf16x8(v[g][i & 1]);
+                q[g][c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xv, wv, q[g][c], 0, 0, 0);
+            }
+        }
+#pragma unroll
+    for (int g = 0; g < kG; ++g) p[g] = q[g][0] + q[g][1];
 }
 
 // Waits for this wave's LDS operations, then the workgroup; loads in flight stay in flight.
@@ -150,7 +181,8 @@ __global__ __launch_bounds__(kFewThreads) void few_gate_up_kernel(FewArgs a) {
     // ---- the ring of weight stages
     u32x4 bw[D][kG][2];
     float sc[D];              // FP8: the scale of this lane's column (gate for columns 0..7, up for 8..15)
-    uint32_t mx[D][kG][2];    // MXFP4: the scale bytes of this lane's row, two blocks
+    uint32_t mx[D];           // MXFP4: the stage's scales, a row and block a lane (mx_row)
+    const int mr = mx_row(lane, kG);
     int iu = (int)blockIdx.x, ib = 0;   // issue cursor: unit, stage of this wave
     int n_units = sh * tiles;  // (the shared expert's, until the routing is known)
     gbytes gp{}, up{};         // this lane's first byte of the unit's gate / up rows
@@ -162,9 +194,10 @@ __global__ __launch_bounds__(kFewThreads) void few_gate_up_kernel(FewArgs a) {
         const size_t at = ((size_t)e * I + n0 + lrow) * row_bytes + (size_t)st0 * 128 + lchunk * 16;
         gp = pick(xg, Xg, Wg) + at;
         up = pick(xg, Xu, Wu) + at;
-        const gbytes s = pick(m < 8, pick(xg, XSg, Sg), pick(xg, XSu, Su));
+        const bool gate = (kFmt == kFewMX ? mr & 8 : m & 8) == 0;
+        const gbytes s = pick(gate, pick(xg, XSg, Sg), pick(xg, XSu, Su));
         if (kFmt == kFewFP8) sp = s + 4 * (((size_t)e * (I / 128) + n0 / 128) * kb_all + st0);
-        if (kFmt == kFewMX) sp = s + ((size_t)e * I + n0 + (m & 7)) * (H / 32);
+        if (kFmt == kFewMX) sp = s + ((size_t)e * I + n0 + 8 * (mr >> 4) + (mr & 7)) * (H / 32);
     };
     // loads of the cursor's stage into slot d, then one step of the cursor; past the last unit the last
     // stage is loaded again (into slots that are not used), so that the loop's loads are unconditional
@@ -181,14 +214,7 @@ __global__ __launch_bounds__(kFewThreads) void few_gate_up_kernel(FewArgs a) {
             bw[d][g][1] = __builtin_nontemporal_load((gvec<u32x4>)(up + at));
         }
         if (kFmt == kFewFP8) sc[d] = *(gvec<float>)(sp + 4 * ib);
-        if (kFmt == kFewMX) {
-#pragma unroll
-            for (int g = 0; g < kG; ++g) {
-                const gbytes row = sp + (size_t)8 * g * (H / 32);
-                mx[d][g][0] = *(gvec<uint32_t>)(row + 4 * kb);
-                mx[d][g][1] = *(gvec<uint32_t>)(row + 4 * min(kb + 1, kb_all - 1));
-            }
-        }
+        if (kFmt == kFewMX) mx[d] = *(gvec<uint32_t>)(sp + 4 * min(kb + (lane & 1), kb_all - 1));
         if (ib + 1 < ns) {
             ++ib;
         } else if (iu + grid < n_units) {
@@ -287,12 +313,12 @@ __global__ __launch_bounds__(kFewThreads) void few_gate_up_kernel(FewArgs a) {
             if (kFmt == kFewMX && i >= 4) at = half ? 2 * H : at;  // (the row's padding: zeros)
             xv[i] = as_bf16x8(*(const u32x4*)&xm[at]);
         }
+        f32x4 p[kG];
+        few_stage<kFmt, kG>(lds, bw[d], lane, kFmt == kFewMX ? mx[d] : 0u, half ? 0u : ~0u, [&](int i) { return xv[i]; }, p);
 #pragma unroll
         for (int g = 0; g < kG; ++g) {
-            const f32x4 p = few_stage<kFmt>(lds, bw[d][g], lane, mx[d][g][0], mx[d][g][1], half ? 0u : ~0u,
-                                            [&](int i) { return xv[i]; });
 #pragma unroll
-            for (int r = 0; r < 4; ++r) acc[g][r] = kFmt == kFewFP8 ? fmaf(p[r], sc[d], acc[g][r]) : acc[g][r] + p[r];
+            for (int r = 0; r < 4; ++r) acc[g][r] = kFmt == kFewFP8 ? fmaf(p[g][r], sc[d], acc[g][r]) : acc[g][r] + p[g][r];
             // the sums are taken here, not where they are next used: a scale that outlived its slot would
             // be copied to another register every round, and that copy would wait for the whole ring
             asm volatile("" : "+v"(acc[g]));
@@ -377,7 +403,7 @@ __global__ __launch_bounds__(kFewThreads) void few_down_kernel(FewArgs a) {
 
     u32x4 bw[D][kG][2], hx[D][F::kNM];
     float sc[D];
-    uint32_t mx[D][kG][2];
+    uint32_t mx[D];
     int iu = 0, is = 0;       // issue cursor: list index, stage of the expert
     gbytes wp{}, hp{}, sp{};  // this lane's weight, activation and scale bytes of the expert
     auto expert_of = [&](int u) {
@@ -392,7 +418,7 @@ __global__ __launch_bounds__(kFewThreads) void few_down_kernel(FewArgs a) {
         hp = Hb + 2 * ((size_t)u * 2 * T + (m < 8 ? t : T + t)) * I;
         const gbytes s = pick(xg, XSd, Sd);
         if (kFmt == kFewFP8) sp = s + 4 * ((size_t)e * (H / 128) + n0 / 128) * kb_all;
-        if (kFmt == kFewMX) sp = s + ((size_t)e * H + n0 + m) * (I / 32);
+        if (kFmt == kFewMX) sp = s + ((size_t)e * H + n0 + mx_row(lane, kG)) * (I / 32);
     };
     int left = 0;  // stages not yet issued
     auto issue = [&](auto tag) {
@@ -414,14 +440,7 @@ __global__ __launch_bounds__(kFewThreads) void few_down_kernel(FewArgs a) {
             hx[d][i] = *(gvec<u32x4>)(hp + 2 * v);
         }
         if (kFmt == kFewFP8) sc[d] = *(gvec<float>)(sp + 4 * is);
-        if (kFmt == kFewMX) {
-#pragma unroll
-            for (int g = 0; g < kG; ++g) {
-                const gbytes row = sp + (size_t)16 * g * (I / 32);
-                mx[d][g][0] = *(gvec<uint32_t>)(row + 4 * kb);
-                mx[d][g][1] = *(gvec<uint32_t>)(row + 4 * min(kb + 1, kb_all - 1));
-            }
-        }
+        if (kFmt == kFewMX) mx[d] = *(gvec<uint32_t>)(sp + 4 * min(kb + (lane & 1), kb_all - 1));
         if (--left > 0) {  // (past the wave's share its last stage is loaded again, into unused slots)
             if (++is == st_e) {
                 is = 0;
@@ -446,12 +465,14 @@ __global__ __launch_bounds__(kFewThreads) void few_down_kernel(FewArgs a) {
         auto compute = [&](auto tag) {
             constexpr int d = decltype(tag)::value;
             const bool half = kFmt == kFewMX && 2 * cs + 1 >= kb_all;
+            f32x4 p[kG];
+            few_stage<kFmt, kG>(lds, bw[d], lane, kFmt == kFewMX ? mx[d] : 0u, half ? 0u : ~0u,
+                                [&](int i) { return as_bf16x8(hx[d][i]); }, p);
 #pragma unroll
             for (int g = 0; g < kG; ++g) {
-                const f32x4 p = few_stage<kFmt>(lds, bw[d][g], lane, mx[d][g][0], mx[d][g][1], half ? 0u : ~0u,
-                                                [&](int i) { return as_bf16x8(hx[d][i]); });
 #pragma unroll
-                for (int r = 0; r < 4; ++r) pe[g][r] = kFmt == kFewFP8 ? fmaf(p[r], sc[d], pe[g][r]) : pe[g][r] + p[r];
+                for (int r = 0; r < 4; ++r)
+                    pe[g][r] = kFmt == kFewFP8 ? fmaf(p[g][r], sc[d], pe[g][r]) : pe[g][r] + p[g][r];
                 asm volatile("" : "+v"(pe[g]));
             }
         };
