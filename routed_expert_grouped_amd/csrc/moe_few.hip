@@ -58,7 +58,8 @@ struct FewArgs {
     int32_t* ids;
     float* wts;
     int32_t* list;
-    uint16_t* h;  // [list index][2 T][I]: hi rows 0..T-1, lo rows T..2T-1
+    uint16_t* h;  // [list index][2 T][pitch]: hi rows 0..T-1, lo rows T..2T-1
+    int pitch;    // I rounded up to 256 (two blocks), the rest zeros
     uint16_t* out;
 };
 
@@ -86,15 +87,18 @@ constexpr int kFewLD = 128 + 16;  // LDS row stride of a stage: conflict-free re
 // each of 2 kG instructions a stage, and bounded the kernel: 284 K of 415 K cycles at 8 tokens.)
 __device__ __forceinline__ int mx_row(int lane, int kG) { return (lane >> 1) & (16 * kG - 1); }
 
-// One stage of kG times 16 weight rows, times the activation fragments x(i): the stage's sums.  Each group
-// goes through the same LDS rows (a wave's LDS operations complete in order), all groups before the first
-// product; the products run in two chains a group, so that a wave has 2 kG independent ones in flight.
+// One stage of kG times 16 weight rows, times the activation fragments x(i).  Each group goes through the
+// same LDS rows (a wave's LDS operations complete in order), all groups before the first product; the
+// products run in two chains a group, so that a wave has 2 kG independent ones in flight.  The chains add
+// to acc; FP8 (post-scaled: acc += stage * sc) starts them at zero.
 // MXFP4: sv holds the stage's scale dwords (four scale bytes, one a quarter, per row and block) as
-// mx_row() says, row r's block b in lane 2 r + b; keep = 0 where the second block is past the end
-// (its weights become zeros, its scale 1).
+// mx_row() says, row r's block b in lane 2 r + b.  The conversion takes its scale operand's exponent
+// field and nothing else, so the quarter's byte is rotated there with its neighbours left in the sign
+// and mantissa.  A last stage of one block has its second block's x as zeros (and the first block's
+// weights again).
 template <int kFmt, int kG, typename X>
-__device__ __forceinline__ void few_stage(uint8_t* lds, const u32x4 (*w)[2], int lane, uint32_t sv, uint32_t keep,
-                                          X&& x, f32x4* p) {
+__device__ __forceinline__ void few_stage(uint8_t* lds, const u32x4 (*w)[2], int lane, uint32_t sv, float sc,
+                                          X&& x, f32x4 (*acc)[2]) {
     using F = FewFmt<kFmt>;
     const int m = lane & 15, kq = lane >> 4;
     const uint8_t* row = lds + m * kFewLD;
@@ -111,19 +115,19 @@ __device__ __forceinline__ void few_stage(uint8_t* lds, const u32x4 (*w)[2], int
     float f[kG][2];
     if (kFmt == kFewMX) {
 #pragma unroll
-        for (int g = 0; g < kG; ++g) {
-            v[g][1] &= keep;
+        for (int g = 0; g < kG; ++g)
 #pragma unroll
             for (int b = 0; b < 2; ++b) {
                 const uint32_t w4 = (uint32_t)__builtin_amdgcn_ds_bpermute(4 * (2 * (16 * g + m) + b), (int)sv);
-                f[g][b] = e8m0_to_f32(((b == 0 || keep ? w4 : 0x7F7F7F7Fu) >> (8 * kq)) & 255u);
+                f[g][b] = __uint_as_float(__builtin_amdgcn_alignbit(w4, w4, (8 * kq + 9) & 31));
             }
-        }
     }
     constexpr int kHalf = F::kNM / 2;
     f32x4 q[kG][2];
 #pragma unroll
-    for (int g = 0; g < kG; ++g) q[g][0] = q[g][1] = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int g = 0; g < kG; ++g)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) q[g][c] = kFmt == kFewFP8 ? f32x4{0.f, 0.f, 0.f, 0.f} : acc[g][c];
 #pragma unroll
     for (int j = 0; j < kHalf; ++j)
 #pragma unroll
@@ -140,7 +144,23 @@ __device__ __forceinline__ void few_stage(uint8_t* lds, const u32x4 (*w)[2], int
             }
         }
 #pragma unroll
-    for (int g = 0; g < kG; ++g) p[g] = q[g][0] + q[g][1];
+    for (int g = 0; g < kG; ++g) {
+        if (kFmt == kFewFP8) {
+#pragma unroll
+            for (int r = 0; r < 4; ++r) acc[g][0][r] = fmaf(q[g][0][r] + q[g][1][r], sc, acc[g][0][r]);
+        } else {
+            acc[g][0] = q[g][0], acc[g][1] = q[g][1];
+        }
+        // the sums are taken here, not where they are next used: a scale that outlived its slot would be
+        // copied to another register every round, and that copy would wait for the whole ring
+        asm volatile("" : "+v"(acc[g][0]), "+v"(acc[g][1]));
+    }
+}
+
+template <int kG>
+__device__ __forceinline__ void few_clear(f32x4 (*acc)[2]) {
+#pragma unroll
+    for (int g = 0; g < kG; ++g) acc[g][0] = acc[g][1] = f32x4{0.f, 0.f, 0.f, 0.f};
 }
 
 // Waits for this wave's LDS operations, then the workgroup; loads in flight stay in flight.
@@ -154,6 +174,7 @@ __global__ __launch_bounds__(kFewThreads) void few_gate_up_kernel(FewArgs a) {
     using F = FewFmt<kFmt>;
     constexpr int D = kFewRing, kCols = 8 * kG;
     __shared__ __attribute__((aligned(16))) uint8_t sX[kFewXBytes];
+    __shared__ __attribute__((aligned(16))) uint8_t sZero[64];
     __shared__ __attribute__((aligned(16))) uint8_t sW[kFewWaves][16 * kFewLD];
     __shared__ float red[2][kFewWaves][kG][32 * 4];
     __shared__ int32_t sids[kFewList];
@@ -185,13 +206,14 @@ __global__ __launch_bounds__(kFewThreads) void few_gate_up_kernel(FewArgs a) {
     const int mr = mx_row(lane, kG);
     int iu = (int)blockIdx.x, ib = 0;   // issue cursor: unit, stage of this wave
     int n_units = sh * tiles;  // (the shared expert's, until the routing is known)
-    gbytes gp{}, up{};         // this lane's first byte of the unit's gate / up rows
-    gbytes sp{};               // its scales
+    gbytes gp{}, up{};         // the unit's gate / up rows, at the wave's part of K (uniform)
+    gbytes sp{};               // this lane's scales
+    const uint32_t wofs = (uint32_t)lrow * (uint32_t)row_bytes + lchunk * 16;  // this lane's bytes of a stage
     auto unit_of = [&](int unit) {  // pointers of a unit
         const int u = unit / tiles, n0 = (unit - u * tiles) * kCols;
         const bool xg = u < sh;
         const int e = xg ? 0 : uniform((int)(list[u - sh] & 0xFFFFu));
-        const size_t at = ((size_t)e * I + n0 + lrow) * row_bytes + (size_t)st0 * 128 + lchunk * 16;
+        const size_t at = ((size_t)e * I + n0) * row_bytes + (size_t)st0 * 128;
         gp = pick(xg, Xg, Wg) + at;
         up = pick(xg, Xu, Wu) + at;
         const bool gate = (kFmt == kFewMX ? mr & 8 : m & 8) == 0;
@@ -203,15 +225,14 @@ __global__ __launch_bounds__(kFewThreads) void few_gate_up_kernel(FewArgs a) {
     // stage is loaded again (into slots that are not used), so that the loop's loads are unconditional
     auto issue = [&](auto tag) {
         constexpr int d = decltype(tag)::value;
-        size_t kofs = (size_t)ib * 128;
         const int kb = 2 * (st0 + ib);  // MXFP4
         // a short last MXFP4 stage: the chunks of the missing block reload the first
-        if (kFmt == kFewMX && kb + 1 >= kb_all && lchunk >= 4) kofs -= 64;
+        const uint32_t ofs = kFmt == kFewMX && kb + 1 >= kb_all && lchunk >= 4 ? wofs - 64 : wofs;
 #pragma unroll
         for (int g = 0; g < kG; ++g) {
-            const size_t at = (size_t)8 * g * row_bytes + kofs;
-            bw[d][g][0] = __builtin_nontemporal_load((gvec<u32x4>)(gp + at));
-            bw[d][g][1] = __builtin_nontemporal_load((gvec<u32x4>)(up + at));
+            const size_t at = (size_t)8 * g * row_bytes + (size_t)ib * 128;
+            bw[d][g][0] = __builtin_nontemporal_load((gvec<u32x4>)(gp + at + ofs));
+            bw[d][g][1] = __builtin_nontemporal_load((gvec<u32x4>)(up + at + ofs));
         }
         if (kFmt == kFewFP8) sc[d] = *(gvec<float>)(sp + 4 * ib);
         if (kFmt == kFewMX) mx[d] = *(gvec<uint32_t>)(sp + 4 * min(kb + (lane & 1), kb_all - 1));
@@ -232,9 +253,9 @@ __global__ __launch_bounds__(kFewThreads) void few_gate_up_kernel(FewArgs a) {
             if (decltype(tag)::value < pre) issue(tag);
         });
     }
-    // ---- x into LDS, rows padded by 16 bytes of zeros (row m starts 4 m banks on)
+    // ---- x into LDS, rows padded by 16 bytes (row m starts 4 m banks on)
     const int xrow = 2 * H + 16, chunks = H / 8;
-    if (tid < T) *(u32x4*)&sX[tid * xrow + 2 * H] = u32x4{0u, 0u, 0u, 0u};
+    if (tid < 4) *(u32x4*)&sZero[16 * tid] = u32x4{0u, 0u, 0u, 0u};
     for (int c = tid; c < T * chunks; c += kFewThreads) {
         const int t = c / chunks, j = c - t * chunks;
         *(u32x4*)&sX[t * xrow + 16 * j] = ((const u32x4*)(a.x + (size_t)t * H))[j];
@@ -299,30 +320,19 @@ __global__ __launch_bounds__(kFewThreads) void few_gate_up_kernel(FewArgs a) {
         __builtin_amdgcn_s_waitcnt(vmcnt_imm(0));
     }
 
-    const uint8_t* xm = sX + (m < T ? m : 0) * xrow;  // rows past the last token repeat token 0 (not stored)
-    f32x4 acc[kG];
-#pragma unroll
-    for (int g = 0; g < kG; ++g) acc[g] = f32x4{0.f, 0.f, 0.f, 0.f};
+    // this lane's x row, at its quarter; rows past the last token repeat token 0 (not stored)
+    const uint8_t* xm = sX + (m < T ? m : 0) * xrow + 2 * F::value(0, kq);
+    f32x4 acc[kG][2];
+    few_clear<kG>(acc);
     auto compute = [&](auto tag, int st) {
         constexpr int d = decltype(tag)::value;
-        const bool half = kFmt == kFewMX && 2 * st + 1 >= kb_all;  // a last stage of one block
+        const uint8_t* x0 = xm + 2 * st * F::kSV;
+        const uint8_t* x1 = kFmt == kFewMX && 2 * st + 1 >= kb_all ? sZero : x0 + 256;  // MXFP4's second block
         bf16x8 xv[F::kNM];
 #pragma unroll
-        for (int i = 0; i < F::kNM; ++i) {
-            int at = 2 * (st * F::kSV + F::value(i, kq));
-            if (kFmt == kFewMX && i >= 4) at = half ? 2 * H : at;  // (the row's padding: zeros)
-            xv[i] = as_bf16x8(*(const u32x4*)&xm[at]);
-        }
-        f32x4 p[kG];
-        few_stage<kFmt, kG>(lds, bw[d], lane, kFmt == kFewMX ? mx[d] : 0u, half ? 0u : ~0u, [&](int i) { return xv[i]; }, p);
-#pragma unroll
-        for (int g = 0; g < kG; ++g) {
-#pragma unroll
-            for (int r = 0; r < 4; ++r) acc[g][r] = kFmt == kFewFP8 ? fmaf(p[g][r], sc[d], acc[g][r]) : acc[g][r] + p[g][r];
-            // the sums are taken here, not where they are next used: a scale that outlived its slot would
-            // be copied to another register every round, and that copy would wait for the whole ring
-            asm volatile("" : "+v"(acc[g]));
-        }
+        for (int i = 0; i < F::kNM; ++i) xv[i] = as_bf16x8(*(const u32x4*)&(i < 4 ? x0 : x1)[16 * (i & 3)]);
+        few_stage<kFmt, kG>(lds, bw[d], lane, kFmt == kFewMX ? mx[d] : 0u, kFmt == kFewFP8 ? sc[d] : 0.0f,
+                            [&](int i) { return xv[i]; }, acc);
     };
     int cu = (int)blockIdx.x, seq = 0;  // the unit being computed
     // Joins the waves' sums of the unit; kG of the waves, in turn, then finish its columns: wave
@@ -330,9 +340,10 @@ __global__ __launch_bounds__(kFewThreads) void few_gate_up_kernel(FewArgs a) {
     auto finish = [&]() {
 #pragma unroll
         for (int g = 0; g < kG; ++g) {
-            if (lane < 32) *(f32x4*)&red[seq & 1][wave][g][4 * lane] = acc[g];  // rows 0..7: lanes 0..31
-            acc[g] = f32x4{0.f, 0.f, 0.f, 0.f};
+            // tokens 0..7 are rows 0..7: lanes 0..31
+            if (lane < 32) *(f32x4*)&red[seq & 1][wave][g][4 * lane] = kFmt == kFewFP8 ? acc[g][0] : acc[g][0] + acc[g][1];
         }
+        few_clear<kG>(acc);
         lds_barrier();
         const int g = (wave - kG * seq) & (kFewWaves - 1);
         if (g < kG) {
@@ -351,9 +362,11 @@ __global__ __launch_bounds__(kFewThreads) void few_gate_up_kernel(FewArgs a) {
             if (mask >> t & 1) {
                 const uint16_t hi = f32_to_bf16(hv);
                 const float rest = hv - bf16_to_f32(hi);
-                uint16_t* h = a.h + ((size_t)u * 2 * T + t) * I + n0 + 8 * g + c;
+                uint16_t* h = a.h + ((size_t)u * 2 * T + t) * a.pitch + n0 + 8 * g + c;
                 h[0] = hi;
-                h[(size_t)T * I] = f32_to_bf16(isfinite(rest) ? rest : 0.0f);
+                h[(size_t)T * a.pitch] = f32_to_bf16(isfinite(rest) ? rest : 0.0f);
+                if (n0 + 8 * g + 8 == I)  // the row's padding
+                    for (int i = 8; I + i <= a.pitch; i += 8) h[i] = h[(size_t)T * a.pitch + i] = 0;
             }
         }
         ++seq;
@@ -405,17 +418,20 @@ __global__ __launch_bounds__(kFewThreads) void few_down_kernel(FewArgs a) {
     float sc[D];
     uint32_t mx[D];
     int iu = 0, is = 0;       // issue cursor: list index, stage of the expert
-    gbytes wp{}, hp{}, sp{};  // this lane's weight, activation and scale bytes of the expert
+    gbytes wp{}, hp{}, sp{};  // the expert's weight rows and h rows (uniform), this lane's scales
+    const uint32_t wofs = (uint32_t)lrow * (uint32_t)row_bytes + lchunk * 16;  // this lane's bytes of a stage
+    uint32_t hofs = 0;        // this lane's h row, at its quarter
     auto expert_of = [&](int u) {
         const uint32_t entry = (uint32_t)uniform((int)list[u]);
         const int id = (int)(entry & 0xFFFF), mask = (int)(entry >> 16);
         const bool xg = id == kFewShared;
         const int e = xg ? 0 : id;
-        wp = pick(xg, Xd, Wd) + ((size_t)e * H + n0 + lrow) * row_bytes + lchunk * 16;
+        wp = pick(xg, Xd, Wd) + ((size_t)e * H + n0) * row_bytes;
         // rows of tokens that are not routed here hold nothing: such a lane reads another's row, and
         // its sums are not taken
         const int t = ((mask >> (m & 7)) & 1) ? (m & 7) : __ffs(mask) - 1;
-        hp = Hb + 2 * ((size_t)u * 2 * T + (m < 8 ? t : T + t)) * I;
+        hp = Hb + 2 * (size_t)u * 2 * T * a.pitch;
+        hofs = 2 * ((uint32_t)(m < 8 ? t : T + t) * (uint32_t)a.pitch + F::value(0, kq));
         const gbytes s = pick(xg, XSd, Sd);
         if (kFmt == kFewFP8) sp = s + 4 * ((size_t)e * (H / 128) + n0 / 128) * kb_all;
         if (kFmt == kFewMX) sp = s + ((size_t)e * H + n0 + mx_row(lane, kG)) * (I / 32);
@@ -424,21 +440,16 @@ __global__ __launch_bounds__(kFewThreads) void few_down_kernel(FewArgs a) {
     auto issue = [&](auto tag) {
         constexpr int d = decltype(tag)::value;
         const int kb = 2 * is;  // MXFP4
-        size_t kofs = (size_t)is * 128;
-        const bool half = kFmt == kFewMX && kb + 1 >= kb_all;  // a last stage of one block
-        if (half && lchunk >= 4) kofs -= 64;
+        const uint32_t ofs = kFmt == kFewMX && kb + 1 >= kb_all && lchunk >= 4 ? wofs - 64 : wofs;
 #pragma unroll
         for (int g = 0; g < kG; ++g)
 #pragma unroll
             for (int i = 0; i < 2; ++i)
                 bw[d][g][i] = __builtin_nontemporal_load(
-                    (gvec<u32x4>)(wp + (size_t)(16 * g + 8 * i) * row_bytes + kofs));
+                    (gvec<u32x4>)(wp + ((size_t)(16 * g + 8 * i) * row_bytes + (size_t)is * 128) + ofs));
 #pragma unroll
-        for (int i = 0; i < F::kNM; ++i) {
-            int v = is * F::kSV + F::value(i, kq);
-            if (half && i >= 4) v -= 128;
-            hx[d][i] = *(gvec<u32x4>)(hp + 2 * v);
-        }
+        for (int i = 0; i < F::kNM; ++i)
+            hx[d][i] = *(gvec<u32x4>)(hp + (2 * is * F::kSV + 2 * F::value(i, 0)) + hofs);
         if (kFmt == kFewFP8) sc[d] = *(gvec<float>)(sp + 4 * is);
         if (kFmt == kFewMX) mx[d] = *(gvec<uint32_t>)(sp + 4 * min(kb + (lane & 1), kb_all - 1));
         if (--left > 0) {  // (past the wave's share its last stage is loaded again, into unused slots)
@@ -448,9 +459,10 @@ __global__ __launch_bounds__(kFewThreads) void few_down_kernel(FewArgs a) {
             }
         }
     };
-    f32x4 acc[kG], pe[kG];  // sums of the experts done, and of the current one
+    f32x4 acc[kG], pe[kG][2];  // sums of the experts done, and of the current one
 #pragma unroll
-    for (int g = 0; g < kG; ++g) acc[g] = pe[g] = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int g = 0; g < kG; ++g) acc[g] = f32x4{0.f, 0.f, 0.f, 0.f};
+    few_clear<kG>(pe);
     if (q0 < q1) {
         iu = q0 / st_e;
         is = q0 - iu * st_e;
@@ -464,17 +476,8 @@ __global__ __launch_bounds__(kFewThreads) void few_down_kernel(FewArgs a) {
         });
         auto compute = [&](auto tag) {
             constexpr int d = decltype(tag)::value;
-            const bool half = kFmt == kFewMX && 2 * cs + 1 >= kb_all;
-            f32x4 p[kG];
-            few_stage<kFmt, kG>(lds, bw[d], lane, kFmt == kFewMX ? mx[d] : 0u, half ? 0u : ~0u,
-                                [&](int i) { return as_bf16x8(hx[d][i]); }, p);
-#pragma unroll
-            for (int g = 0; g < kG; ++g) {
-#pragma unroll
-                for (int r = 0; r < 4; ++r)
-                    pe[g][r] = kFmt == kFewFP8 ? fmaf(p[g][r], sc[d], pe[g][r]) : pe[g][r] + p[g][r];
-                asm volatile("" : "+v"(pe[g]));
-            }
+            few_stage<kFmt, kG>(lds, bw[d], lane, kFmt == kFewMX ? mx[d] : 0u, kFmt == kFewFP8 ? sc[d] : 0.0f,
+                                [&](int i) { return as_bf16x8(hx[d][i]); }, pe);
         };
         auto flush = [&]() {  // the expert's sums, for the tokens routed to it (a wave's share may
                               // begin or end inside an expert)
@@ -483,11 +486,9 @@ __global__ __launch_bounds__(kFewThreads) void few_down_kernel(FewArgs a) {
             for (int r = 0; r < 4; ++r) {
                 const bool mine = (mask >> ((4 * kq + r) & 7)) & 1;
 #pragma unroll
-                for (int g = 0; g < kG; ++g) {
-                    acc[g][r] += mine ? pe[g][r] : 0.0f;
-                    pe[g][r] = 0.0f;
-                }
+                for (int g = 0; g < kG; ++g) acc[g][r] += mine ? pe[g][0][r] + pe[g][1][r] : 0.0f;
             }
+            few_clear<kG>(pe);
         };
         ring_loop<D>(q1 - q0, [&](auto tag) {
             compute(tag);
@@ -528,9 +529,11 @@ static moe_status check_few(int32_t T, int32_t k, const moe_expert_weights* w) {
     return MOE_OK;
 }
 
+static int few_pitch(int I) { return (I + 255) & ~255; }
+
 static size_t few_ws(int T, int k, const moe_expert_weights* w) {
     const size_t experts = std::min<int64_t>((int64_t)T * k, w->n_groups) + 1;  // and the shared one
-    return T == 0 ? 0 : kFewHead + experts * 2 * T * (size_t)w->I * sizeof(uint16_t);
+    return T == 0 ? 0 : kFewHead + experts * 2 * T * (size_t)few_pitch(w->I) * sizeof(uint16_t);
 }
 
 template <int kFmt>
@@ -596,6 +599,7 @@ extern "C" moe_status moe_layer_few(const float* scores, const uint16_t* x, int3
     a.wts = topk_w;
     a.list = static_cast<int32_t*>(ws);
     a.h = reinterpret_cast<uint16_t*>(static_cast<uint8_t*>(ws) + kFewHead);
+    a.pitch = few_pitch(w->I);
     a.out = out;
     hipStream_t st = as_stream(stream);
     switch (w->dtype) {
