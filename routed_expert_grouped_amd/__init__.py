@@ -354,48 +354,57 @@ def moe_expert_ffn_a8(x, k: int, perm, offsets, w: MoeExpertWeights, y=None, ws=
     return y, ws
 
 
-def _want(call, device, **tensors):
-    """Checks what a call takes of its tensors: name=(tensor or None, dtype, shape).  Raw pointers
-    are passed on, so a wrong layout would be read as another one."""
+def _off(t, dtype, shape, index):
+    """Whether a tensor is not what a call takes: raw pointers are passed on, so another layout would
+    be read as this one.  (None is an argument left out.)"""
+    return t is not None and (t.dtype is not dtype or t.shape != shape or t.get_device() != index
+                              or not t.is_contiguous())
+
+
+def _refuse(call, index, **tensors):
+    """Names the argument that _off found: name=(tensor, dtype, shape)."""
     for name, (t, dtype, shape) in tensors.items():
-        if t is None:
-            continue
-        if t.dtype != dtype or t.shape != shape or not t.is_contiguous() or t.device != device:
+        if _off(t, dtype, shape, index):
             raise ValueError(f"{call}: {name} must be a contiguous {dtype} tensor of shape "
-                             f"{tuple(shape)} on {device}, not {t.dtype} {tuple(t.shape)} with strides "
-                             f"{t.stride()} on {t.device}")
+                             f"{tuple(shape)} on cuda:{index}, not {t.dtype} {tuple(t.shape)} with "
+                             f"strides {t.stride()} on {t.device}")
+    raise AssertionError(call)
 
 
-class _On:
-    """The device and stream of one call: torch's current stream of the tensors' device (also when
-    another device is current), or the caller's `stream`.  Buffers that a call allocates itself
-    belong to that stream."""
+def _where(call, t, stream):
+    """(device index, stream handle) of a call on tensor t: torch's current stream of t's device, or the
+    caller's `stream`, which must be of that device."""
+    index = t.get_device()
+    if index < 0:
+        raise ValueError(f"{call}: the tensors must be on a GPU, not on {t.device}")
+    if stream is None:
+        return index, torch._C._cuda_getCurrentRawStream(index)
+    if stream.device_index != index:
+        raise ValueError(f"{call}: the stream is of {stream.device}, the tensors are on {t.device}")
+    return index, stream.cuda_stream
 
-    def __init__(self, call, device, stream):
-        if device.type != "cuda":
-            raise ValueError(f"{call}: the tensors must be on a GPU, not on {device}")
-        if stream is None:
-            stream = torch.cuda.current_stream(device)
-            self.other = None
-        elif stream.device != device:
-            raise ValueError(f"{call}: the stream is of {stream.device}, the tensors are on {device}")
-        else:
-            self.other = stream
-        self.device, self.stream = device, ctypes.c_void_p(stream.cuda_stream)
-        self.current = device.index == torch.cuda.current_device()
 
-    def empty(self, shape, dtype):
-        if self.other is None:
-            return torch.empty(shape, dtype=dtype, device=self.device)
-        with torch.cuda.stream(self.other):
-            return torch.empty(shape, dtype=dtype, device=self.device)
+def _new(t, stream, shape, dtype):
+    """A buffer on t's device that belongs to the stream the call runs on."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=t.device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=t.device)
 
-    def run(self, call, *args):
-        if self.current:
-            _check(call, getattr(lib(), call)(*args, self.stream))
-        else:
-            with torch.cuda.device(self.device):
-                _check(call, getattr(lib(), call)(*args, self.stream))
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _run(call, index, *args):
+    """The C call, with the tensors' device current (it launches there)."""
+    if index == torch._C._cuda_getDevice():
+        status = getattr(_lib or lib(), call)(*args)
+    else:
+        with torch.cuda.device(index):
+            status = getattr(_lib or lib(), call)(*args)
+    if status != MOE_OK:
+        raise MoeError(call, status)
 
 
 def moe_rmsnorm_quantize_act(x, weight, residual=None, eps: float = 1e-6, normed=True,
@@ -408,7 +417,9 @@ def moe_rmsnorm_quantize_act(x, weight, residual=None, eps: float = 1e-6, normed
     call = "moe_rmsnorm_quantize_act"
     if x.dim() != 2:
         raise ValueError(f"{call}: x must have two dimensions")
-    on, (rows, K) = _On(call, x.device, stream), x.shape
+    dev, st = _where(call, x, stream)
+    shape, b16 = x.shape, torch.int16
+    rows, K = shape
     if quantized:
         pitch = exps.shape[1] if exps is not None else exp_pitch(K) if pitch is None else pitch
     else:
@@ -418,20 +429,23 @@ def moe_rmsnorm_quantize_act(x, weight, residual=None, eps: float = 1e-6, normed
         y = None
     if residual is None and sum_out is not None:
         raise ValueError(f"{call}: sum_out needs a residual")
-    shape, b16 = x.shape, torch.int16
-    _want(call, x.device, x=(x, b16, shape), weight=(weight, b16, (K,)),
-          residual=(residual, b16, shape), sum_out=(sum_out, b16, shape), y=(y, b16, shape),
-          codes=(codes, torch.uint8, shape), exps=(exps, torch.int8, (rows, pitch)))
+    u8, i8 = torch.uint8, torch.int8
+    if (_off(x, b16, shape, dev) or _off(weight, b16, (K,), dev) or _off(residual, b16, shape, dev)
+            or _off(sum_out, b16, shape, dev) or _off(y, b16, shape, dev) or _off(codes, u8, shape, dev)
+            or _off(exps, i8, (rows, pitch), dev)):
+        _refuse(call, dev, x=(x, b16, shape), weight=(weight, b16, (K,)), residual=(residual, b16, shape),
+                sum_out=(sum_out, b16, shape), y=(y, b16, shape), codes=(codes, u8, shape),
+                exps=(exps, i8, (rows, pitch)))
     if residual is not None and sum_out is None:
-        sum_out = on.empty(shape, b16)
+        sum_out = _new(x, stream, shape, b16)
     if normed and y is None:
-        y = on.empty(shape, b16)
+        y = _new(x, stream, shape, b16)
     if quantized and codes is None:
-        codes = on.empty(shape, torch.uint8)
+        codes = _new(x, stream, shape, u8)
     if quantized and exps is None:
-        exps = on.empty((rows, pitch), torch.int8)
-    on.run(call, _p(x), _p(residual), _p(weight), rows, K, eps, _p(sum_out), _p(y), _p(codes),
-           _p(exps), pitch)
+        exps = _new(x, stream, (rows, pitch), i8)
+    _run(call, dev, x.data_ptr(), _ptr(residual), weight.data_ptr(), rows, K, eps, _ptr(sum_out), _ptr(y),
+         _ptr(codes), _ptr(exps), pitch, st)
     return sum_out, y, codes, exps
 
 
@@ -448,17 +462,19 @@ def moe_router_scores(x, w, scores=None, ws=None, stream=None):
     call = "moe_router_scores"
     if x.dim() != 2 or w.dim() != 2 or w.dtype not in (torch.int16, torch.float32):
         raise ValueError(f"{call}: x [T, H] and w [E, H] (torch.int16 or torch.float32) are wanted")
-    on, (T, H), E = _On(call, x.device, stream), x.shape, w.shape[0]
-    _want(call, x.device, x=(x, torch.int16, x.shape), w=(w, w.dtype, (E, H)),
-          scores=(scores, torch.float32, (T, E)),
-          ws=(ws, torch.uint8, None if ws is None else (ws.numel(),)))
+    dev, st = _where(call, x, stream)
+    (T, H), E, f32 = x.shape, w.shape[0], torch.float32
+    if (_off(x, torch.int16, (T, H), dev) or _off(w, w.dtype, (E, H), dev)
+            or _off(scores, f32, (T, E), dev) or (ws is not None and _off(ws, torch.uint8, (ws.numel(),), dev))):
+        _refuse(call, dev, x=(x, torch.int16, (T, H)), w=(w, w.dtype, (E, H)), scores=(scores, f32, (T, E)),
+                ws=(ws, torch.uint8, None if ws is None else (ws.numel(),)))
     if scores is None:
-        scores = on.empty((T, E), torch.float32)
+        scores = _new(x, stream, (T, E), f32)
     if ws is None and T > 16:
         need = moe_router_scores_workspace_size(T, H, E)
-        ws = on.empty((need,), torch.uint8) if need else None
-    on.run(call, _p(x), T, H, _p(w), MOE_ROUTER_W_F32 if w.dtype == torch.float32 else MOE_ROUTER_W_BF16,
-           E, _p(scores), _p(ws), 0 if ws is None else ws.numel())
+        ws = _new(x, stream, (need,), torch.uint8) if need else None
+    _run(call, dev, x.data_ptr(), T, H, w.data_ptr(), MOE_ROUTER_W_F32 if w.dtype is f32 else MOE_ROUTER_W_BF16,
+         E, scores.data_ptr(), _ptr(ws), 0 if ws is None else ws.numel(), st)
     return scores
 
 
@@ -468,13 +484,17 @@ def moe_linear_a8(codes, exps, w, s_w, y=None, stream=None):
     call = "moe_linear_a8"
     if codes.dim() != 2 or w.dim() != 2 or exps.dim() != 2:
         raise ValueError(f"{call}: codes [M, K], exps [M, pitch] and w [N, K] are wanted")
-    on, (M, K), N = _On(call, codes.device, stream), codes.shape, w.shape[0]
-    _want(call, codes.device, codes=(codes, torch.uint8, (M, K)), exps=(exps, torch.int8, (M, exps.shape[1])),
-          w=(w, torch.uint8, (N, K)), s_w=(s_w, torch.float32, (-(-N // 128), K // 128)),
-          y=(y, torch.int16, (M, N)))
+    dev, st = _where(call, codes, stream)
+    (M, K), N, pitch, u8, i8 = codes.shape, w.shape[0], exps.shape[1], torch.uint8, torch.int8
+    blocks = (-(-N // 128), K // 128)
+    if (_off(codes, u8, (M, K), dev) or _off(exps, i8, (M, pitch), dev) or _off(w, u8, (N, K), dev)
+            or _off(s_w, torch.float32, blocks, dev) or _off(y, torch.int16, (M, N), dev)):
+        _refuse(call, dev, codes=(codes, u8, (M, K)), exps=(exps, i8, (M, pitch)), w=(w, u8, (N, K)),
+                s_w=(s_w, torch.float32, blocks), y=(y, torch.int16, (M, N)))
     if y is None:
-        y = on.empty((M, N), torch.int16)
-    on.run(call, _p(codes), _p(exps), exps.shape[1], M, N, K, _p(w), _p(s_w), _p(y))
+        y = _new(codes, stream, (M, N), torch.int16)
+    _run(call, dev, codes.data_ptr(), exps.data_ptr(), pitch, M, N, K, w.data_ptr(), s_w.data_ptr(),
+         y.data_ptr(), st)
     return y
 
 
@@ -496,25 +516,28 @@ def moe_layer_few(scores, x, k: int, w: MoeExpertWeights, shared=None, score_fn=
     call = "moe_layer_few"
     if x.dim() != 2 or scores.dim() != 2:
         raise ValueError(f"{call}: scores [T, E] and x [T, H] are wanted")
-    on, (T, H) = _On(call, x.device, stream), x.shape
+    dev, st = _where(call, x, stream)
+    (T, H), E, i32, f32, b16 = x.shape, w.n_groups, torch.int32, torch.float32, torch.int16
     if H != w.H:
         raise ValueError(f"{call}: x has rows of {H}, the weights take {w.H}")
-    _want(call, x.device, scores=(scores, torch.float32, (T, w.n_groups)), x=(x, torch.int16, x.shape),
-          topk_ids=(topk_ids, torch.int32, (T, k)), topk_w=(topk_w, torch.float32, (T, k)),
-          out=(out, torch.int16, x.shape),
-          work=(work, torch.uint8, None if work is None else (work.numel(),)))
+    if (_off(scores, f32, (T, E), dev) or _off(x, b16, (T, H), dev) or _off(topk_ids, i32, (T, k), dev)
+            or _off(topk_w, f32, (T, k), dev) or _off(out, b16, (T, H), dev)
+            or (work is not None and _off(work, torch.uint8, (work.numel(),), dev))):
+        _refuse(call, dev, scores=(scores, f32, (T, E)), x=(x, b16, (T, H)), topk_ids=(topk_ids, i32, (T, k)),
+                topk_w=(topk_w, f32, (T, k)), out=(out, b16, (T, H)),
+                work=(work, torch.uint8, None if work is None else (work.numel(),)))
     fn = SCORE_FN[score_fn] if isinstance(score_fn, str) else int(score_fn)
     if topk_ids is None:
-        topk_ids = on.empty((T, k), torch.int32)
+        topk_ids = _new(x, stream, (T, k), i32)
     if topk_w is None:
-        topk_w = on.empty((T, k), torch.float32)
+        topk_w = _new(x, stream, (T, k), f32)
     if out is None:
-        out = on.empty((T, H), torch.int16)
+        out = _new(x, stream, (T, H), b16)
     if work is None:
-        work = on.empty((moe_layer_few_workspace_size(T, k, w),), torch.uint8)
-    on.run(call, _p(scores), _p(x), T, k, fn, int(renorm), ctypes.byref(w),
-           None if shared is None else ctypes.byref(shared), _p(topk_ids), _p(topk_w), _p(out), _p(work),
-           work.numel())
+        work = _new(x, stream, (moe_layer_few_workspace_size(T, k, w),), torch.uint8)
+    _run(call, dev, scores.data_ptr(), x.data_ptr(), T, k, fn, int(renorm), ctypes.byref(w),
+         None if shared is None else ctypes.byref(shared), topk_ids.data_ptr(), topk_w.data_ptr(),
+         out.data_ptr(), work.data_ptr(), work.numel(), st)
     return out, topk_ids, topk_w
 
 
