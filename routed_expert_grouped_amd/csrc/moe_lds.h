@@ -33,6 +33,11 @@ __device__ __forceinline__ void lds_dma4(const void* src, const void* lds) {
                  : "memory", "m0");
 }
 
+// LDS byte address of a shared array.
+__device__ __forceinline__ uint32_t lds_address(const void* lds) {
+    return (uint32_t)(size_t)(const __attribute__((address_space(3))) void*)lds;
+}
+
 // The same two loads with the LDS byte address given directly (a wave-uniform value).
 __device__ __forceinline__ void lds_dma16_at(const void* src, uint32_t lds) {
     asm volatile("s_mov_b32 m0, %1\n\tglobal_load_lds_dwordx4 %0, off"

@@ -202,16 +202,17 @@ __global__ __launch_bounds__(kWM * kWN * 64) void linear_tile_kernel(LinArgs a) 
         ep[i] = (gbytes)a.e + (size_t)min(m0 + (wm * kMI + i) * 32 + fr, a.M - 1) * a.pitch;
     const int sg = min(n0 + wn * 32 * kNI, a.N - 1) / 128;  // (columns past the end are not stored)
     const gbytes sp = (gbytes)a.s + 4 * (size_t)sg * kb_all;
+    const uint32_t la = lds_address(sA), lb = lds_address(sB);
     int en[kMI];
     float sn;
     auto issue = [&](int kb) {
         const int buf = kb & 1;
 #pragma unroll
         for (int i = 0; i < kIA; ++i)
-            lds_dma16((const void*)(ap[i] + (size_t)kb * 128), &sA[buf][8 * (kIA * wave + i) * 128]);
+            lds_dma16_at((const void*)(ap[i] + (size_t)kb * 128), la + (buf * BM + 8 * (kIA * wave + i)) * 128);
 #pragma unroll
         for (int i = 0; i < kIB; ++i)
-            lds_dma16((const void*)(bp[i] + (size_t)kb * 128), &sB[buf][8 * (kIB * wave + i) * 128]);
+            lds_dma16_at((const void*)(bp[i] + (size_t)kb * 128), lb + (buf * BN + 8 * (kIB * wave + i)) * 128);
         // the block's scales, to registers: complete with the direct loads, at the next step's wait
 #pragma unroll
         for (int i = 0; i < kMI; ++i) en[i] = *(gvec<int8_t>)(ep[i] + kb);

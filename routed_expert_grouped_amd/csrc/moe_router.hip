@@ -8,15 +8,19 @@
 //   few tokens  one workgroup per expert (and per group of up to 8 tokens): its four waves read the
 //               expert's row once, each lane multiplies its chunks with every token's, and the lanes'
 //               sums are joined in a fixed order.  W's bytes and the launch bound it.
-//   many tokens 128 x 128 tiles on the matrix cores (32x32x16 bf16), operands through LDS.  When
-//               the tiles alone do not fill the chip, K is split over workgroups into fp32 partial
-//               scores in the caller's workspace, and a second launch adds them in order.
+//   more        tiles on the matrix cores (32x32x16 bf16), operands through LDS.  When the tiles alone
+//               do not fill the chip, K is split over workgroups into fp32 partial scores in the
+//               caller's workspace, and a second launch adds them in order.  Up to a few thousand tokens
+//               64 x 64 tiles staged through registers; above, 128 x 256 or 128 x 128 tiles loaded directly
+//               to LDS, three stages deep.
 //
 // fp32 W goes to the matrix cores as three bf16 parts, w = hi + mid + lo (8 + 8 + 8 significand bits:
-// exact for every finite w whose parts are not subnormal), so no bits of W are lost.
+// exact for every finite w whose parts are not subnormal), so no bits of W are lost.  The small tiles split
+// it while staging; for the large ones a launch before writes the parts to the workspace.
 #include "libmoe.h"
 #include "moe_device.h"
 #include "moe_host.h"
+#include "moe_lds.h"
 
 #include <algorithm>
 
@@ -84,27 +88,40 @@ __global__ __launch_bounds__(kDotThreads) void router_dot_kernel(const uint16_t*
     }
 }
 
-// 128 x 128 tile, four waves of 64 x 64 each, K in steps of 64.  The next step's operands are loaded to
-// registers before the current step's products and written to the other LDS buffer after them, one
-// barrier a step (fp32 W, three planes of it, has room for one buffer and takes two barriers).
-constexpr int kRtM = 128, kRtN = 128, kRtK = 64;
+// The three bf16 parts of two floats (a in the low halves): an infinity or a NaN is all in the first.
+__device__ __forceinline__ void split3(float a, float b, uint32_t* parts) {
+#pragma unroll
+    for (int p = 0; p < 3; ++p) {
+        const uint32_t v = f32x2_to_bf16x2(a, b);
+        parts[p] = v;
+        const float ha = __uint_as_float(v << 16), hb = __uint_as_float(v & 0xffff0000u);
+        a = isfinite(ha) ? a - ha : 0.0f;
+        b = isfinite(hb) ? b - hb : 0.0f;
+    }
+}
+
+// 64 x 64 tile, four waves of 32 x 32, K in steps of 64.  The next step's operands are loaded to registers
+// before the current step's products and written to the other LDS buffer after them, one barrier a step
+// (fp32 W: one buffer of three planes, two barriers).
+constexpr int kRtK = 64;
 constexpr int kRtLd = kRtK * 2 + 16;  // LDS row bytes: 16 consecutive rows' 16-byte reads hit distinct banks
 
 template <bool kF32>
-__global__ __launch_bounds__(256, 2) void router_gemm_kernel(const uint16_t* __restrict__ x, int T,
-                                                             int H, const void* __restrict__ w, int E,
-                                                             int n_tiles, int tiles, int splits,
-                                                             float* __restrict__ out) {
-    constexpr int kPlanes = kF32 ? 3 : 1, kBufs = kF32 ? 1 : 2;
-    __shared__ __attribute__((aligned(16))) uint8_t sA[kBufs][kRtM * kRtLd];
-    __shared__ __attribute__((aligned(16))) uint8_t sB[kBufs][kPlanes][kRtN * kRtLd];
+__global__ __launch_bounds__(256) void router_gemm_kernel(const uint16_t* __restrict__ x, int T, int H,
+                                                          const void* __restrict__ w, int E, int n_tiles,
+                                                          int tiles, int splits, float* __restrict__ out) {
+    constexpr int kMI = 1, kNI = 1;
+    constexpr int kPlanes = kF32 ? 3 : 1, kBufs = kF32 ? 1 : 2, kM = 64 * kMI, kN = 64 * kNI;
+    constexpr int kLA = kM / 32, kLB = kN / 32, kWB = kF32 ? 2 : 1;  // staging loads a thread, 16-byte words of 8 weights
+    __shared__ __attribute__((aligned(16))) uint8_t sA[kBufs][kM * kRtLd];
+    __shared__ __attribute__((aligned(16))) uint8_t sB[kBufs][kPlanes][kN * kRtLd];
     // consecutive workgroups go to the 8 XCDs in turn: XCD i takes the contiguous range i of logical
     // tiles, so that the column tiles of a row tile share its x rows in one L2
     const int R8 = (tiles * splits + 7) / 8;
     const int L = ((int)blockIdx.x & 7) * R8 + ((int)blockIdx.x >> 3);
     if (L >= tiles * splits) return;
     const int split = L / tiles, tile = L - split * tiles;
-    const int m0 = tile / n_tiles * kRtM, n0 = tile % n_tiles * kRtN;
+    const int m0 = tile / n_tiles * kM, n0 = tile % n_tiles * kN;
     const int steps_all = (H + kRtK - 1) / kRtK;
     const int k0 = (int)((int64_t)steps_all * split / splits), k1 = (int)((int64_t)steps_all * (split + 1) / splits);
 
@@ -113,43 +130,35 @@ __global__ __launch_bounds__(256, 2) void router_gemm_kernel(const uint16_t* __r
     // staging: thread loads 16-byte chunk tid % 8 of rows tid / 8 + 32 i; rows past the end read the last
     // row (not stored), chunks past H are zeros (both operands: 0 times garbage could be NaN)
     const int lc = tid & 7, lr = tid >> 3;
-    const uint16_t* ap[4];
-    const char* bp[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        ap[i] = x + (size_t)min(m0 + lr + 32 * i, T - 1) * H;
-        bp[i] = (const char*)w + (size_t)min(n0 + lr + 32 * i, E - 1) * H * (kF32 ? 4 : 2);
-    }
-    u32x4 ra[4], rb[4][kF32 ? 2 : 1];
+    u32x4 ra[kLA], rb[kLB][kWB];
     auto load = [&](int step) {
         const int c = step * (kRtK / 8) + lc;
         const bool in = c < H / 8;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            ra[i] = in ? ((const u32x4*)ap[i])[c] : u32x4{0u, 0u, 0u, 0u};
+        for (int i = 0; i < kLA; ++i)
+            ra[i] = in ? ((const u32x4*)(x + (size_t)min(m0 + lr + 32 * i, T - 1) * H))[c] : u32x4{0u, 0u, 0u, 0u};
 #pragma unroll
-            for (int p = 0; p < (kF32 ? 2 : 1); ++p)
-                rb[i][p] = in ? ((const u32x4*)bp[i])[kF32 ? 2 * c + p : c] : u32x4{0u, 0u, 0u, 0u};
+        for (int i = 0; i < kLB; ++i) {
+            const char* row = (const char*)w + (size_t)min(n0 + lr + 32 * i, E - 1) * H * (kF32 ? 4 : 2);
+#pragma unroll
+            for (int p = 0; p < kWB; ++p)
+                rb[i][p] = in ? ((const u32x4*)row)[kWB * c + p] : u32x4{0u, 0u, 0u, 0u};
         }
     };
     auto stage = [&](int buf) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < kLA; ++i) *(u32x4*)&sA[buf][(lr + 32 * i) * kRtLd + lc * 16] = ra[i];
+#pragma unroll
+        for (int i = 0; i < kLB; ++i) {
             const int at = (lr + 32 * i) * kRtLd + lc * 16;
-            *(u32x4*)&sA[buf][at] = ra[i];
             if constexpr (kF32) {
                 u32x4 pl[3];
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    float a = __uint_as_float(rb[i][j >> 1][(2 * j) & 3]), b = __uint_as_float(rb[i][j >> 1][(2 * j + 1) & 3]);
+                    uint32_t q[3];
+                    split3(__uint_as_float(rb[i][j >> 1][(2 * j) & 3]), __uint_as_float(rb[i][j >> 1][(2 * j + 1) & 3]), q);
 #pragma unroll
-                    for (int p = 0; p < 3; ++p) {
-                        const uint32_t v = f32x2_to_bf16x2(a, b);
-                        pl[p][j] = v;
-                        const float ha = __uint_as_float(v << 16), hb = __uint_as_float(v & 0xffff0000u);
-                        a = isfinite(ha) ? a - ha : 0.0f;  // an infinity or a NaN is all in the first part
-                        b = isfinite(hb) ? b - hb : 0.0f;
-                    }
+                    for (int p = 0; p < 3; ++p) pl[p][j] = q[p];
                 }
 #pragma unroll
                 for (int p = 0; p < 3; ++p) *(u32x4*)&sB[buf][p][at] = pl[p];
@@ -158,30 +167,30 @@ __global__ __launch_bounds__(256, 2) void router_gemm_kernel(const uint16_t* __r
             }
         }
     };
-    f32x16 acc[2][2];
+    f32x16 acc[kMI][kNI];
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
+    for (int i = 0; i < kMI; ++i)
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
+        for (int j = 0; j < kNI; ++j)
 #pragma unroll
             for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.0f;
     auto compute = [&](int buf) {
 #pragma unroll
         for (int ks = 0; ks < kRtK / 16; ++ks) {
-            bf16x8 fa[2];
+            bf16x8 fa[kMI];
 #pragma unroll
-            for (int i = 0; i < 2; ++i)
-                fa[i] = as_bf16x8(*(const u32x4*)&sA[buf][(wm * 64 + i * 32 + fr) * kRtLd + ks * 32 + half * 16]);
+            for (int i = 0; i < kMI; ++i)
+                fa[i] = as_bf16x8(*(const u32x4*)&sA[buf][((wm * kMI + i) * 32 + fr) * kRtLd + ks * 32 + half * 16]);
 #pragma unroll
             for (int p = kPlanes - 1; p >= 0; --p) {  // the small parts first
-                bf16x8 fb[2];
+                bf16x8 fb[kNI];
 #pragma unroll
-                for (int j = 0; j < 2; ++j)
-                    fb[j] = as_bf16x8(*(const u32x4*)&sB[buf][p][(wn * 64 + j * 32 + fr) * kRtLd + ks * 32 + half * 16]);
+                for (int j = 0; j < kNI; ++j)
+                    fb[j] = as_bf16x8(*(const u32x4*)&sB[buf][p][((wn * kNI + j) * 32 + fr) * kRtLd + ks * 32 + half * 16]);
 #pragma unroll
-                for (int i = 0; i < 2; ++i)
+                for (int i = 0; i < kMI; ++i)
 #pragma unroll
-                    for (int j = 0; j < 2; ++j)
+                    for (int j = 0; j < kNI; ++j)
                         acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fa[i], fb[j], acc[i][j], 0, 0, 0);
             }
         }
@@ -202,34 +211,193 @@ __global__ __launch_bounds__(256, 2) void router_gemm_kernel(const uint16_t* __r
     // D layout: value v of a lane is row 8 (v / 4) + 4 half + v % 4, column fr
     float* o = out + (size_t)split * T * E;
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
+    for (int i = 0; i < kMI; ++i)
 #pragma unroll
         for (int v = 0; v < 16; ++v) {
-            const int t = m0 + wm * 64 + i * 32 + 8 * (v >> 2) + 4 * half + (v & 3);
+            const int t = m0 + (wm * kMI + i) * 32 + 8 * (v >> 2) + 4 * half + (v & 3);
             if (t >= T) continue;
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                const int e = n0 + wn * 64 + j * 32 + fr;
+            for (int j = 0; j < kNI; ++j) {
+                const int e = n0 + (wn * kNI + j) * 32 + fr;
                 if (e < E) o[(size_t)t * E + e] = acc[i][j][v];
             }
         }
 }
 
+// fp32 W to its three bf16 parts [3][E][H]
+__global__ __launch_bounds__(256) void router_split_kernel(const float* __restrict__ w, int64_t chunks,
+                                                           uint16_t* __restrict__ parts) {
+    const int64_t c = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (c >= chunks) return;
+    float v[8];
+    load_w8<true>(w, (int)c, v);
+    u32x4 pl[3];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        uint32_t q[3];
+        split3(v[2 * j], v[2 * j + 1], q);
+#pragma unroll
+        for (int p = 0; p < 3; ++p) pl[p][j] = q[p];
+    }
+#pragma unroll
+    for (int p = 0; p < 3; ++p) ((u32x4*)parts)[p * chunks + c] = pl[p];
+}
+
+__device__ const u32x4 kRouterZeros = {0u, 0u, 0u, 0u};
+
+// 128 x (32 kNI kWN) tile, eight waves, K in stages of 64 and (fp32 W) of one of its planes, the small
+// parts first: stage s is K step s / planes.  Operand rows are 128 bytes in LDS, eight 16-byte chunks, chunk
+// c at slot c ^ ((row >> 1) & 7), so that 16 consecutive rows' reads of one chunk fall in distinct banks.
+// Loads go directly to LDS, two stages ahead in three buffers, 2 + kNI kWN / 2 a wave and stage; a stage
+// waits until only the next one's are in flight.  Rows past the end read the last row (not stored), chunks
+// past H read zeros.
+template <int kMI, int kNI, int kWM, int kWN>
+__global__ __launch_bounds__(512) void router_dma_kernel(const uint16_t* __restrict__ x, int T, int H,
+                                                         const uint16_t* __restrict__ w, int planes, int E,
+                                                         int n_tiles, int tiles, int splits,
+                                                         float* __restrict__ out) {
+    constexpr int kM = 32 * kMI * kWM, kN = 32 * kNI * kWN, kIA = kM / 64, kIB = kN / 64;
+    static_assert(kWM * kWN == 8 && kM == 128, "eight waves, 128 rows");
+    __shared__ __attribute__((aligned(1024))) uint8_t sA[3][kM * 128];
+    __shared__ __attribute__((aligned(1024))) uint8_t sB[3][kN * 128];
+    const int R8 = (tiles * splits + 7) / 8;
+    const int L = ((int)blockIdx.x & 7) * R8 + ((int)blockIdx.x >> 3);
+    if (L >= tiles * splits) return;
+    const int split = L / tiles, tile = L - split * tiles;
+    const int m0 = tile / n_tiles * kM, n0 = tile % n_tiles * kN;
+    const int steps = (H + kRtK - 1) / kRtK * planes;
+    const int k0 = (int)((int64_t)steps * split / splits), k1 = (int)((int64_t)steps * (split + 1) / splits);
+
+    const int lane = lane_id(), wave = uniform((int)threadIdx.x >> 6);
+    const int wm = wave / kWN, wn = wave % kWN, fr = lane & 31, half = lane >> 5;
+    const char *ap[kIA], *bp[kIB];
+    int ac[kIA], bc[kIB];  // the chunks this lane loads
+#pragma unroll
+    for (int i = 0; i < kIA; ++i) {
+        const int r = 8 * (kIA * wave + i) + (lane >> 3);
+        ac[i] = (lane & 7) ^ ((r >> 1) & 7);
+        ap[i] = (const char*)(x + (size_t)min(m0 + r, T - 1) * H + 8 * ac[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < kIB; ++i) {
+        const int r = 8 * (kIB * wave + i) + (lane >> 3);
+        bc[i] = (lane & 7) ^ ((r >> 1) & 7);
+        bp[i] = (const char*)(w + (size_t)min(n0 + r, E - 1) * H + 8 * bc[i]);
+    }
+    const size_t plane_bytes = (size_t)E * H * 2;
+    int step = k0 / planes, plane = planes - 1 - k0 % planes;  // of the next stage to load
+    const uint32_t la = lds_address(sA), lb = lds_address(sB);
+    auto issue = [&](int buf) {
+        const size_t at = (size_t)step * 128, bt = at + plane * plane_bytes;
+        const int left = H / 8 - 8 * step;  // chunks of this step
+        if (left >= 8) {
+#pragma unroll
+            for (int i = 0; i < kIA; ++i) lds_dma16_at(ap[i] + at, la + (buf * kM + 8 * (kIA * wave + i)) * 128);
+#pragma unroll
+            for (int i = 0; i < kIB; ++i) lds_dma16_at(bp[i] + bt, lb + (buf * kN + 8 * (kIB * wave + i)) * 128);
+        } else {
+            const char* zeros = (const char*)&kRouterZeros;
+#pragma unroll
+            for (int i = 0; i < kIA; ++i)
+                lds_dma16_at(ac[i] < left ? ap[i] + at : zeros, la + (buf * kM + 8 * (kIA * wave + i)) * 128);
+#pragma unroll
+            for (int i = 0; i < kIB; ++i)
+                lds_dma16_at(bc[i] < left ? bp[i] + bt : zeros, lb + (buf * kN + 8 * (kIB * wave + i)) * 128);
+        }
+        if (--plane < 0) {
+            plane = planes - 1;
+            ++step;
+        }
+    };
+    f32x16 acc[kMI][kNI];
+#pragma unroll
+    for (int i = 0; i < kMI; ++i)
+#pragma unroll
+        for (int j = 0; j < kNI; ++j)
+#pragma unroll
+            for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.0f;
+    auto frag = [&](const uint8_t* t, int row, int c) {
+        return as_bf16x8(*(const u32x4*)&t[row * 128 + ((c ^ ((row >> 1) & 7)) << 4)]);
+    };
+    issue(0);
+    if (k0 + 1 < k1) issue(1);
+    int buf = 0;
+    for (int s = k0; s < k1; ++s) {
+        if (s + 1 < k1) __builtin_amdgcn_s_waitcnt(vmcnt_imm(kIA + kIB));
+        else __builtin_amdgcn_s_waitcnt(vmcnt_imm(0));
+        __syncthreads();  // stage s is in LDS, and every wave has left stage s - 1's buffer
+        if (s + 2 < k1) issue(buf == 0 ? 2 : buf - 1);
+#pragma unroll
+        for (int ks = 0; ks < kRtK / 16; ++ks) {
+            bf16x8 fa[kMI], fb[kNI];
+#pragma unroll
+            for (int i = 0; i < kMI; ++i) fa[i] = frag(sA[buf], (wm * kMI + i) * 32 + fr, 2 * ks + half);
+#pragma unroll
+            for (int j = 0; j < kNI; ++j) fb[j] = frag(sB[buf], (wn * kNI + j) * 32 + fr, 2 * ks + half);
+#pragma unroll
+            for (int i = 0; i < kMI; ++i)
+#pragma unroll
+                for (int j = 0; j < kNI; ++j)
+                    acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fa[i], fb[j], acc[i][j], 0, 0, 0);
+        }
+        buf = buf == 2 ? 0 : buf + 1;
+    }
+    float* o = out + (size_t)split * T * E;
+#pragma unroll
+    for (int i = 0; i < kMI; ++i)
+#pragma unroll
+        for (int v = 0; v < 16; ++v) {
+            const int t = m0 + (wm * kMI + i) * 32 + 8 * (v >> 2) + 4 * half + (v & 3);
+            if (t >= T) continue;
+#pragma unroll
+            for (int j = 0; j < kNI; ++j) {
+                const int e = n0 + (wn * kNI + j) * 32 + fr;
+                if (e < E) o[(size_t)t * E + e] = acc[i][j][v];
+            }
+        }
+}
+
+// The parts' sums, in part order, eight loads in flight.
 __global__ __launch_bounds__(256) void router_join_kernel(const float* __restrict__ part, int64_t n,
                                                           int splits, float* __restrict__ scores) {
     const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
     if (i >= n) return;
-    float s = part[i];
-    for (int k = 1; k < splits; ++k) s += part[(size_t)k * n + i];
+    float s = 0.0f;
+    int k = 0;
+    for (; k + 8 <= splits; k += 8) {
+        float v[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = part[(size_t)(k + j) * n + i];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) s += v[j];
+    }
+    for (; k < splits; ++k) s += part[(size_t)k * n + i];
     scores[i] = s;
 }
 
-// K splits of the tile kernel: enough workgroups for two on every CU, at least four K steps each
-static int router_splits(int T, int H, int E) {
-    const int64_t tiles = (int64_t)((T + kRtM - 1) / kRtM) * ((E + kRtN - 1) / kRtN);
+// Which tiles T tokens take, and into how many parts K goes.
+struct RouterPlan {
+    bool dma;
+    int kM, kN, n_tiles, tiles, splits;
+    size_t w_bytes, part_bytes;  // workspace: fp32 W's parts, then the partial scores
+};
+
+constexpr int kRouterDmaT = 2048;
+
+static RouterPlan router_plan(int T, int H, int E, bool f32) {
+    RouterPlan p{};
+    p.dma = T >= kRouterDmaT;
+    p.kM = p.dma ? 128 : 64;
+    // 256 columns, or 128 where the last 256 would be half empty
+    p.kN = !p.dma ? 64 : (E + 127) / 128 % 2 == 0 ? 256 : 128;
+    p.n_tiles = (E + p.kN - 1) / p.kN;
+    p.tiles = (T + p.kM - 1) / p.kM * p.n_tiles;
+    // one round of workgroups (two a CU of the small tiles), at least four K steps each
     const int steps = (H + kRtK - 1) / kRtK;
-    const int64_t want = 512 / std::max<int64_t>(1, tiles);
-    return (int)std::max<int64_t>(1, std::min<int64_t>(want, steps / 4));
+    p.splits = std::max(1, std::min((p.dma ? 256 : 512) / p.tiles, steps / 4));
+    p.w_bytes = p.dma && f32 ? ((size_t)3 * E * H * 2 + 255) & ~size_t(255) : 0;
+    p.part_bytes = p.splits > 1 ? (size_t)p.splits * T * E * sizeof(float) : 0;
+    return p;
 }
 
 static moe_status check_router(int32_t T, int32_t H, int32_t E, int32_t w_dtype) {
@@ -240,10 +408,10 @@ static moe_status check_router(int32_t T, int32_t H, int32_t E, int32_t w_dtype)
     return MOE_OK;
 }
 
-static size_t router_ws(int T, int H, int E) {
+static size_t router_ws(int T, int H, int E, bool f32) {
     if (T <= kRouterDotT) return 0;
-    const int s = router_splits(T, H, E);
-    return s > 1 ? (size_t)s * T * E * sizeof(float) : 0;
+    const RouterPlan p = router_plan(T, H, E, f32);
+    return p.w_bytes + p.part_bytes;
 }
 
 }  // namespace moe
@@ -254,7 +422,7 @@ extern "C" moe_status moe_router_scores_workspace_size(int32_t T, int32_t H, int
     if (!bytes) return MOE_ERR_INVALID_ARG;
     const moe_status s = check_router(T, H, E, MOE_ROUTER_W_BF16);
     if (s != MOE_OK) return s;
-    *bytes = router_ws(T, H, E);
+    *bytes = std::max(router_ws(T, H, E, false), router_ws(T, H, E, true));
     return MOE_OK;
 }
 
@@ -265,11 +433,11 @@ extern "C" moe_status moe_router_scores(const uint16_t* x, int32_t T, int32_t H,
     if (s != MOE_OK || T == 0) return s;
     if (!x || !w || !scores || !aligned16(x) || !aligned16(w) || !aligned16(scores))
         return MOE_ERR_INVALID_ARG;
-    const size_t need = router_ws(T, H, E);
+    const bool f32 = w_dtype == MOE_ROUTER_W_F32;
+    const size_t need = router_ws(T, H, E, f32);
     if (need && (!ws || ws_bytes < need)) return MOE_ERR_WORKSPACE;
     if (need && !aligned16(ws)) return MOE_ERR_INVALID_ARG;
     hipStream_t st = as_stream(stream);
-    const bool f32 = w_dtype == MOE_ROUTER_W_F32;
     if (T <= kRouterDotT) {
         const int TT = T == 1 ? 1 : T == 2 ? 2 : T <= 4 ? 4 : 8;
         const dim3 grid((unsigned)E, (unsigned)((T + TT - 1) / TT)), block(kDotThreads);
@@ -282,16 +450,33 @@ extern "C" moe_status moe_router_scores(const uint16_t* x, int32_t T, int32_t H,
 #undef MOE_DOT
         return launch_status();
     }
-    const int splits = router_splits(T, H, E);
-    const int n_tiles = (E + kRtN - 1) / kRtN, tiles = (T + kRtM - 1) / kRtM * n_tiles;
-    const int64_t wgs = ((int64_t)tiles * splits + 7) & ~int64_t(7);
-    float* o = splits > 1 ? (float*)ws : scores;
-    const dim3 grid((unsigned)wgs), block(256);
-    if (f32) router_gemm_kernel<true><<<grid, block, 0, st>>>(x, T, H, w, E, n_tiles, tiles, splits, o);
-    else router_gemm_kernel<false><<<grid, block, 0, st>>>(x, T, H, w, E, n_tiles, tiles, splits, o);
+    const RouterPlan p = router_plan(T, H, E, f32);
+    const int splits = p.splits;
+    float* part = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + p.w_bytes);
+    float* o = splits > 1 ? part : scores;
+    const dim3 grid((unsigned)(((int64_t)p.tiles * splits + 7) & ~int64_t(7)));
+    if (p.dma) {
+        const uint16_t* wb = static_cast<const uint16_t*>(w);
+        if (f32) {
+            uint16_t* parts = static_cast<uint16_t*>(ws);
+            const int64_t chunks = (int64_t)E * H / 8;
+            router_split_kernel<<<dim3((unsigned)((chunks + 255) / 256)), dim3(256), 0, st>>>(
+                static_cast<const float*>(w), chunks, parts);
+            wb = parts;
+        }
+        const int planes = f32 ? 3 : 1;
+        if (p.kN == 256)
+            router_dma_kernel<2, 2, 2, 4><<<grid, dim3(512), 0, st>>>(x, T, H, wb, planes, E, p.n_tiles, p.tiles, splits, o);
+        else
+            router_dma_kernel<1, 2, 4, 2><<<grid, dim3(512), 0, st>>>(x, T, H, wb, planes, E, p.n_tiles, p.tiles, splits, o);
+    } else if (f32) {
+        router_gemm_kernel<true><<<grid, dim3(256), 0, st>>>(x, T, H, w, E, p.n_tiles, p.tiles, splits, o);
+    } else {
+        router_gemm_kernel<false><<<grid, dim3(256), 0, st>>>(x, T, H, w, E, p.n_tiles, p.tiles, splits, o);
+    }
     moe_status r = launch_status();
     if (r != MOE_OK || splits == 1) return r;
     const int64_t n = (int64_t)T * E;
-    router_join_kernel<<<dim3((unsigned)((n + 255) / 256)), dim3(256), 0, st>>>((const float*)ws, n, splits, scores);
+    router_join_kernel<<<dim3((unsigned)((n + 255) / 256)), dim3(256), 0, st>>>(part, n, splits, scores);
     return launch_status();
 }
