@@ -53,4 +53,12 @@ __device__ __forceinline__ void lds_dma4_at(const void* src, uint32_t lds) {
                  : "memory", "m0");
 }
 
+// One direct global -> LDS load of 16 bytes per lane from a uniform base and a byte offset per lane.
+__device__ __forceinline__ void lds_dma16_from(const void* base, uint32_t offset, uint32_t lds) {
+    asm volatile("s_mov_b32 m0, %2\n\tglobal_load_lds_dwordx4 %0, %1"
+                 :
+                 : "v"(offset), "s"((uint64_t)base), "s"(__builtin_amdgcn_readfirstlane(lds))
+                 : "memory", "m0");
+}
+
 }  // namespace moe

@@ -168,67 +168,84 @@ __global__ __launch_bounds__(kLinWaves * 64) void linear_stream_kernel(LinArgs a
     }
 }
 
-// kMI x kNI subtiles of 32 x 32 a wave, kWM x kWN waves.
+// kMI x 2 subtiles of 32 x 32 a wave, kWM x kWN waves.
+//
 // LDS rows are 128 bytes (one block's codes), eight 16-byte chunks, chunk c at slot c ^ ((row >> 1) & 7):
 // 16 consecutive rows' reads of one chunk fall in distinct banks.  32x32x64 operands: lane l holds row
 // l % 32, chunks 4 j + l / 32 and 4 j + 2 + l / 32 of half j of the block (both operands alike).
-template <int kMI, int kNI, int kWM, int kWN>
+//
+// A block's sum must leave the matrix cores to be scaled (16 fused multiply-adds a subtile, half the matrix
+// cores' time if they waited for each other), and its operands come from LDS.  So every wave runs three
+// things at once: subtile t's two products, subtile t - 1's multiply-adds between them, and the LDS reads
+// of later subtiles.  The last row of subtiles of a step reads the next step's first operands: the step's
+// barrier stands before it, when all of this step's operands are in registers (the loads of the step
+// after next go to the buffer that it frees) and the next step's have landed.
+template <int kMI, int kWM, int kWN>
 __global__ __launch_bounds__(kWM * kWN * 64) void linear_tile_kernel(LinArgs a) {
-    constexpr int kWaves = kWM * kWN, BM = 32 * kMI * kWM, BN = 32 * kNI * kWN;
+    constexpr int kNI = 2, kWaves = kWM * kWN, BM = 32 * kMI * kWM, BN = 32 * kNI * kWN;
     constexpr int kIA = BM / 8 / kWaves, kIB = BN / 8 / kWaves;  // direct loads a wave a step (8 rows each)
-    static_assert(32 * kNI <= 128 && 128 % (32 * kNI) == 0, "one weight scale a wave");
+    static_assert(kMI == 2 || kMI == 4, "the last row of subtiles follows the barrier");
     __shared__ __attribute__((aligned(1024))) uint8_t sA[2][BM * 128];
     __shared__ __attribute__((aligned(1024))) uint8_t sB[2][BN * 128];
+    __shared__ uint8_t sE[2][BM * 16];
+    __shared__ float sS[2][BN / 128 * 16];
     int mt, nt;
     if (!lin_tile<8>(a, mt, nt)) return;
     const int lane = lane_id(), wave = uniform((int)threadIdx.x >> 6);
     const int wm = wave / kWN, wn = wave % kWN, fr = lane & 31, half = lane >> 5;
-    const int K = a.K, kb_all = K / 128, m0 = mt * BM, n0 = nt * BN;
+    const int K = a.K, kb_all = K / 128, m0 = uniform(mt * BM), n0 = uniform(nt * BN);
 
-    gbytes ap[kIA], bp[kIB];
-#pragma unroll
-    for (int i = 0; i < kIA; ++i) {
-        const int r = 8 * (kIA * wave + i) + (lane >> 3);
-        ap[i] = (gbytes)a.a + (size_t)min(m0 + r, a.M - 1) * K + (((lane & 7) ^ ((r >> 1) & 7)) << 4);
-    }
-#pragma unroll
-    for (int i = 0; i < kIB; ++i) {
-        const int r = 8 * (kIB * wave + i) + (lane >> 3);
-        bp[i] = (gbytes)a.w + (size_t)min(n0 + r, a.N - 1) * K + (((lane & 7) ^ ((r >> 1) & 7)) << 4);
-    }
-    gbytes ep[kMI];
-#pragma unroll
-    for (int i = 0; i < kMI; ++i)
-        ep[i] = (gbytes)a.e + (size_t)min(m0 + (wm * kMI + i) * 32 + fr, a.M - 1) * a.pitch;
-    const int sg = min(n0 + wn * 32 * kNI, a.N - 1) / 128;  // (columns past the end are not stored)
-    const gbytes sp = (gbytes)a.s + 4 * (size_t)sg * kb_all;
-    const uint32_t la = lds_address(sA), lb = lds_address(sB);
-    int en[kMI];
-    float sn;
+    // direct loads: from the tile's first row, at a byte offset per lane (rows past the end: the last row)
+    const uint8_t *ab = a.a + (size_t)m0 * K, *bb = a.w + (size_t)n0 * K;
+    const uint32_t la = lds_address(sA) + 8 * kIA * wave * 128, lb = lds_address(sB) + 8 * kIB * wave * 128;
     auto issue = [&](int kb) {
-        const int buf = kb & 1;
+        const uint32_t buf = kb & 1;
+        // (the offsets are made here: eight registers held over a step would be eight too many)
+        int l = lane;
+        asm volatile("" : "+v"(l));
+        auto offset = [&](int r, int last) { return __umul24(min(r, last), K) + (((l & 7) ^ ((r >> 1) & 7)) << 4); };
 #pragma unroll
         for (int i = 0; i < kIA; ++i)
-            lds_dma16_at((const void*)(ap[i] + (size_t)kb * 128), la + (buf * BM + 8 * (kIA * wave + i)) * 128);
+            lds_dma16_from(ab + (size_t)kb * 128, offset(8 * (kIA * wave + i) + (l >> 3), a.M - 1 - m0),
+                           la + buf * (BM * 128) + i * 1024);
 #pragma unroll
         for (int i = 0; i < kIB; ++i)
-            lds_dma16_at((const void*)(bp[i] + (size_t)kb * 128), lb + (buf * BN + 8 * (kIB * wave + i)) * 128);
-        // the block's scales, to registers: complete with the direct loads, at the next step's wait
-#pragma unroll
-        for (int i = 0; i < kMI; ++i) en[i] = *(gvec<int8_t>)(ep[i] + kb);
-        sn = *(gvec<float>)(sp + 4 * kb);
+            lds_dma16_from(bb + (size_t)kb * 128, offset(8 * (kIB * wave + i) + (l >> 3), a.N - 1 - n0),
+                           lb + buf * (BN * 128) + i * 1024);
     };
-    int arow[kMI], brow[kNI];
-#pragma unroll
-    for (int i = 0; i < kMI; ++i) arow[i] = (wm * kMI + i) * 32 + fr;
-#pragma unroll
-    for (int i = 0; i < kNI; ++i) brow[i] = (wn * kNI + i) * 32 + fr;
-    auto frag = [&](const uint8_t* s, int row, int j) {
-        const int x = (row >> 1) & 7;
-        return lin_join(*(const u32x4*)&s[row * 128 + (((4 * j + half) ^ x) << 4)],
-                        *(const u32x4*)&s[row * 128 + (((4 * j + 2 + half) ^ x) << 4)]);
+    // the tile's scales, 16 blocks at a time in two buffers: E8M0 bytes of the rows, fp32 of the 128-column
+    // groups (registers hold none of them over a step)
+    auto window = [&](int w) {
+        int tid = (int)threadIdx.x;
+        asm volatile("" : "+v"(tid));  // (nothing of this is kept in registers from one window to the next)
+#pragma unroll 1
+        for (int i = tid; i < BM * 16; i += kWaves * 64)
+            sE[w & 1][i] = (uint8_t)(a.e[(size_t)min(m0 + (i >> 4), a.M - 1) * a.pitch + min(16 * w + (i & 15), kb_all - 1)] + 127);
+        if (tid < BN / 128 * 16)
+            sS[w & 1][tid] = a.s[(size_t)(min(n0 + 128 * (tid >> 4), a.N - 1) / 128) * kb_all + min(16 * w + (tid & 15), kb_all - 1)];
     };
-    f32x16 acc[kMI][kNI];
+    // this lane's LDS chunks: rows 32 apart have the same swizzle; half j's chunks 4 j + half, 4 j + 2 + half
+    const uint32_t c0 = fr * 128 + ((half ^ ((fr >> 1) & 7)) << 4);
+    auto frag = [&](const uint8_t* t, int j) {
+        return lin_join(*(const u32x4*)&t[c0 ^ (64 * j)], *(const u32x4*)&t[c0 ^ (64 * j + 32)]);
+    };
+    i32x8 fa[2], fb[kNI][2];  // halves of the current subtile row of A, and of B
+    int ea[2];                // block scales of subtile rows i and i + 1
+    auto read_e = [&](auto tag, int kb) {
+        constexpr int i = decltype(tag)::value;
+        ea[i & 1] = sE[(kb >> 4) & 1][((wm * kMI + i) * 32 + fr) * 16 + (kb & 15)];
+    };
+    auto read_a = [&](auto tag, int j, int kb) {
+        constexpr int i = decltype(tag)::value;
+        fa[j] = frag(sA[kb & 1] + (wm * kMI + i) * 32 * 128, j);
+    };
+    auto read_b = [&](auto tag, int kb) {
+        constexpr int i = decltype(tag)::value;
+#pragma unroll
+        for (int j = 0; j < 2; ++j) fb[i][j] = frag(sB[kb & 1] + (wn * kNI + i) * 32 * 128, j);
+    };
+    auto scale_of = [&](int kb) { return sS[(kb >> 4) & 1][(wn * 32 * kNI / 128) * 16 + (kb & 15)]; };
+    f32x16 acc[kMI][kNI], p[2];
 #pragma unroll
     for (int i = 0; i < kMI; ++i)
 #pragma unroll
@@ -236,39 +253,66 @@ __global__ __launch_bounds__(kWM * kWN * 64) void linear_tile_kernel(LinArgs a) 
 #pragma unroll
             for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.0f;
     const f32x16 zero = {};
+    p[1] = zero;
+    float s = 0.0f, sl = 0.0f;  // the step's weight scale, and the scale of the subtile before
+    auto take = [&](auto tag, int v0, float scale) {  // half of subtile t's multiply-adds
+        constexpr int t = decltype(tag)::value;
+#pragma unroll
+        for (int v = 0; v < 8; ++v)
+            acc[t / kNI][t % kNI][v0 + v] = fmaf(p[t & 1][v0 + v], scale, acc[t / kNI][t % kNI][v0 + v]);
+        // (taken here: the compiler would otherwise move products and sums past the barrier to their next
+        // use, and hold every operand of the step in registers until then)
+        asm volatile("" : "+v"(acc[t / kNI][t % kNI]));
+    };
+    constexpr int kT = kMI * kNI;  // subtiles a step: even, so that subtile -1 is kT - 1 of the step before
+    static_assert(kT % 2 == 0, "p alternates over steps too");
+    auto subtile = [&](auto tag, int kb) {
+        constexpr int t = decltype(tag)::value, i = t / kNI, j = t % kNI;
+        using prev = std::integral_constant<int, (t + kT - 1) % kT>;
+        // a half of A is read for the next subtile row (the last row: of the next step; after the last step
+        // nothing uses it) when its last product is issued, one product before its first use
+        using next = std::integral_constant<int, (i + 1) % kMI>;
+        const int kn = i + 1 == kMI ? kb + 1 : kb;
+        const float scale = t == 0 ? sl : s;
+        p[t & 1] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(fa[0], fb[j][0], zero, 0, 0, 0, ea[i & 1], 0, kLinE8M0One);
+        __builtin_amdgcn_sched_barrier(0);
+        if constexpr (j == 0) read_e(next{}, kn);
+        if constexpr (j == kNI - 1) read_a(next{}, 0, kn);
+        take(prev{}, 0, scale);
+        __builtin_amdgcn_sched_barrier(0);
+        p[t & 1] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(fa[1], fb[j][1], p[t & 1], 0, 0, 0, ea[i & 1], 0, kLinE8M0One);
+        __builtin_amdgcn_sched_barrier(0);
+        if constexpr (j == kNI - 1) read_a(next{}, 1, kn);
+        if constexpr (i + 1 == kMI) read_b(std::integral_constant<int, j>{}, kb + 1);
+        take(prev{}, 8, scale);
+        __builtin_amdgcn_sched_barrier(0);
+    };
     issue(0);
+    window(0);
+    __builtin_amdgcn_s_waitcnt(vmcnt_imm(0));
+    __syncthreads();
+    if (kb_all > 1) issue(1);
+    read_e(std::integral_constant<int, 0>{}, 0);
+    read_a(std::integral_constant<int, 0>{}, 0, 0);
+    read_a(std::integral_constant<int, 0>{}, 1, 0);
+    read_b(std::integral_constant<int, 0>{}, 0);
+    read_b(std::integral_constant<int, 1>{}, 0);
+    s = scale_of(0);
     for (int kb = 0; kb < kb_all; ++kb) {
+        if ((kb & 15) == 8 && (kb | 15) + 1 < kb_all) window(kb / 16 + 1);
+        each_slot<kT - kNI>([&](auto tag) { subtile(tag, kb); });
+        // every wave has this step's operands in registers, and the next step's codes are in LDS
         __builtin_amdgcn_s_waitcnt(vmcnt_imm(0));
-        __syncthreads();  // step kb is in LDS, and every wave has left step kb - 1's buffer
-        int ec[kMI];
-#pragma unroll
-        for (int i = 0; i < kMI; ++i) ec[i] = en[i] + 127;
-        const float s = sn;
-        if (kb + 1 < kb_all) issue(kb + 1);
-        const uint8_t *A = sA[kb & 1], *B = sB[kb & 1];
-        i32x8 fb[kNI][2];
-#pragma unroll
-        for (int j = 0; j < kNI; ++j)
-#pragma unroll
-            for (int h = 0; h < 2; ++h) fb[j][h] = frag(B, brow[j], h);
-#pragma unroll
-        for (int i = 0; i < kMI; ++i) {
-            i32x8 fa[2];
-#pragma unroll
-            for (int h = 0; h < 2; ++h) fa[h] = frag(A, arow[i], h);
-            f32x16 p[kNI];
-#pragma unroll
-            for (int j = 0; j < kNI; ++j)
-                p[j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(fa[0], fb[j][0], zero, 0, 0, 0, ec[i], 0, kLinE8M0One);
-#pragma unroll
-            for (int j = 0; j < kNI; ++j)
-                p[j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(fa[1], fb[j][1], p[j], 0, 0, 0, ec[i], 0, kLinE8M0One);
-#pragma unroll
-            for (int j = 0; j < kNI; ++j)
-#pragma unroll
-                for (int v = 0; v < 16; ++v) acc[i][j][v] = fmaf(p[j][v], s, acc[i][j][v]);
-        }
+        __syncthreads();
+        if (kb + 2 < kb_all) issue(kb + 2);
+        const float next = scale_of(kb + 1);
+        subtile(std::integral_constant<int, kT - 2>{}, kb);
+        subtile(std::integral_constant<int, kT - 1>{}, kb);
+        sl = s;
+        s = next;
     }
+    take(std::integral_constant<int, kT - 1>{}, 0, sl);
+    take(std::integral_constant<int, kT - 1>{}, 8, sl);
     // D layout: value v of a lane is row 8 (v / 4) + 4 half + v % 4, column fr
 #pragma unroll
     for (int i = 0; i < kMI; ++i)
@@ -317,6 +361,6 @@ extern "C" moe_status moe_linear_a8(const uint8_t* x_codes, const int8_t* x_exps
     if (M <= 32) return lin_launch(a, 32, 16, kLinWaves * 64, linear_stream_kernel<2>, st);
     if (M <= kLinStreamM) return lin_launch(a, 64, 16, kLinWaves * 64, linear_stream_kernel<4>, st);
     const int64_t large = ((int64_t)(M + 255) / 256) * ((N + 255) / 256);
-    if (large >= 192) return lin_launch(a, 256, 256, 512, linear_tile_kernel<4, 2, 2, 4>, st);
-    return lin_launch(a, 128, 128, 256, linear_tile_kernel<2, 2, 2, 2>, st);
+    if (large >= 192) return lin_launch(a, 256, 256, 512, linear_tile_kernel<4, 2, 4>, st);
+    return lin_launch(a, 128, 128, 256, linear_tile_kernel<2, 2, 2>, st);
 }
