@@ -65,105 +65,142 @@ __device__ __forceinline__ bool lin_tile(const LinArgs& a, int& mt, int& nt) {
     return true;
 }
 
-constexpr int kLinWaves = 8, kLinRing = 4;
+constexpr int kLinWaves = 8;
 constexpr int kLinLD = 128 + 16;  // LDS row stride of a wave's 16 weight rows
 
-// MT row tiles of 16
-template <int MT>
+// MT row tiles of 16, kG groups of 16 columns: a weight stage meets MT row tiles and an activation stage kG
+// column groups, so a wave reads MT + kG tiles' bytes for MT kG tiles' products.
+template <int MT, int kG>
 __global__ __launch_bounds__(kLinWaves * 64) void linear_stream_kernel(LinArgs a) {
-    constexpr int D = kLinRing;
+    constexpr int D = MT + kG <= 4 ? 4 : MT + kG == 5 ? 3 : 2;  // stages in flight, within the registers
     __shared__ __attribute__((aligned(16))) uint8_t sW[kLinWaves][16 * kLinLD];
-    __shared__ int8_t sE[MT * 16][kLinMaxBlocks];
-    __shared__ f32x4 red[kLinWaves][MT][kWave];
+    __shared__ int8_t sE[MT * 16][kLinMaxBlocks + 4];  // (padded: 16 rows' bytes of a block in as many banks)
+    __shared__ f32x4 red[kLinWaves][kG][kWave];
     int mt, nt;
     if (!lin_tile<16>(a, mt, nt)) return;
     const int tid = (int)threadIdx.x, lane = lane_id(), wave = uniform(tid >> 6);
     const int m = lane & 15, q = lane >> 4;
-    const int K = a.K, kb_all = K / 128, m0 = mt * MT * 16, n0 = nt * 16;
+    const int K = a.K, kb_all = K / 128, m0 = mt * MT * 16, n0 = nt * 16 * kG;
     const int st0 = kb_all * wave / kLinWaves, ns = kb_all * (wave + 1) / kLinWaves - st0;
     uint8_t* lds = sW[wave];
 
-    // weights: instruction i loads rows 8 i + lane / 8, 16-byte chunk lane % 8 (whole 128-byte lines);
-    // activations: row m of each tile, chunks q and q + 4 (the operand layout: which K a chunk holds
-    // does not matter as long as both operands agree)
-    const gbytes W = held(a.w), A = held(a.a);
-    gbytes wp[2], xp[MT];
+    // Instruction i of a 16-row tile of either operand loads rows 8 i + lane / 8, 16-byte chunk lane % 8: whole
+    // 128-byte lines, 16 cache accesses.  (Straight to the operand layout, a row a lane, it would be 64:
+    // the cache's tags then bounded 64 x 2048 x 7168 at 22 us.)  Both operands change layout through the
+    // wave's LDS rows; lane quarter q takes chunks q and q + 4 (which K a chunk holds does not matter as
+    // long as both operands agree).  Offsets from the tile's first row and the wave's first block.
+    const gbytes W = held(a.w + (size_t)n0 * K + (size_t)st0 * 128), A = held(a.a + (size_t)m0 * K + (size_t)st0 * 128);
+    uint32_t wo[kG][2], xo[MT][2];
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
-        wp[i] = W + (size_t)min(n0 + 8 * i + (lane >> 3), a.N - 1) * K + (size_t)st0 * 128 + (lane & 7) * 16;
+    for (int g = 0; g < kG; ++g)
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            wo[g][i] = __umul24(min(16 * g + 8 * i + (lane >> 3), a.N - 1 - n0), K) + (lane & 7) * 16;
 #pragma unroll
     for (int t = 0; t < MT; ++t)
-        xp[t] = A + (size_t)min(m0 + 16 * t + m, a.M - 1) * K + (size_t)st0 * 128 + q * 16;
-    const gbytes sp = held(a.s) + 4 * ((size_t)(n0 / 128) * kb_all + st0);
-    u32x4 bw[D][2], ax[D][MT][2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            xo[t][i] = __umul24(min(16 * t + 8 * i + (lane >> 3), a.M - 1 - m0), K) + (lane & 7) * 16;
+    // (16 kG divides 128: one scale row for all groups)
+    const gbytes sp = held(a.s + (size_t)(n0 / 128) * kb_all + st0);
+    u32x4 bw[D][kG][2], ax[D][MT][2];
     float sc[D];
     int is = 0;
     auto issue = [&](auto tag) {  // past the wave's part its last block is loaded again (not used)
         constexpr int d = decltype(tag)::value;
         const size_t at = (size_t)is * 128;
 #pragma unroll
-        for (int i = 0; i < 2; ++i) bw[d][i] = __builtin_nontemporal_load((gvec<u32x4>)(wp[i] + at));
+        for (int g = 0; g < kG; ++g)
 #pragma unroll
-        for (int t = 0; t < MT; ++t) {
-            ax[d][t][0] = *(gvec<u32x4>)(xp[t] + at);
-            ax[d][t][1] = *(gvec<u32x4>)(xp[t] + at + 64);
-        }
-        sc[d] = *(gvec<float>)(sp + 4 * is);
+            for (int i = 0; i < 2; ++i) bw[d][g][i] = __builtin_nontemporal_load((gvec<u32x4>)(W + at + wo[g][i]));
+#pragma unroll
+        for (int t = 0; t < MT; ++t)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) ax[d][t][i] = *(gvec<u32x4>)(A + at + xo[t][i]);
+        sc[d] = *(gvec<float>)(sp + 4 * (size_t)is);
         is = min(is + 1, ns - 1);
     };
-    // block exponents of the workgroup's rows, all of K
-    for (int i = tid; i < MT * 16 * kb_all; i += kLinWaves * 64) {
-        const int r = i / kb_all, b = i - r * kb_all;
-        sE[r][b] = a.e[(size_t)min(m0 + r, a.M - 1) * a.pitch + b];
-    }
-    __syncthreads();
-    f32x4 acc[MT];
-#pragma unroll
-    for (int t = 0; t < MT; ++t) acc[t] = f32x4{0.f, 0.f, 0.f, 0.f};
-    if (ns > 0) {
-        // (in slot order, as the loop has them: the waits count on it)
+    // the first stages (in slot order, as the loop has them: the waits count on it), then the block
+    // exponents of the workgroup's rows, all of K, eight loads in flight a thread
+    if (ns > 0)
         each_slot<D>([&](auto tag) {
             issue(tag);
             __builtin_amdgcn_sched_barrier(0);
         });
+    const int n_e = MT * 16 * kb_all;
+    for (int i0 = tid; i0 < n_e; i0 += 8 * kLinWaves * 64) {
+        int8_t v[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const int i = min(i0 + j * kLinWaves * 64, n_e - 1), r = i / kb_all;
+            v[j] = a.e[(size_t)min(m0 + r, a.M - 1) * a.pitch + (i - r * kb_all)];
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const int i = i0 + j * kLinWaves * 64, r = i / kb_all;
+            if (i < n_e) sE[r][i - r * kb_all] = v[j];
+        }
+    }
+    __syncthreads();
+    f32x4 acc[MT][kG];
+#pragma unroll
+    for (int t = 0; t < MT; ++t)
+#pragma unroll
+        for (int g = 0; g < kG; ++g) acc[t][g] = f32x4{0.f, 0.f, 0.f, 0.f};
+    if (ns > 0) {
         int kb = st0;
         ring_loop<D>(ns, [&](auto tag) {
             constexpr int d = decltype(tag)::value;
+            auto turn = [&](const u32x4* v) {  // all through the same rows: a wave's LDS operations complete in order
 #pragma unroll
-            for (int i = 0; i < 2; ++i)
-                *(u32x4*)&lds[(8 * i + (lane >> 3)) * kLinLD + (lane & 7) * 16] = bw[d][i];
-            __builtin_amdgcn_wave_barrier();  // (a wave's LDS operations complete in order)
-            const i32x8 fb = lin_join(*(const u32x4*)&lds[m * kLinLD + q * 16],
-                                      *(const u32x4*)&lds[m * kLinLD + 64 + q * 16]);
+                for (int i = 0; i < 2; ++i) *(u32x4*)&lds[(8 * i + (lane >> 3)) * kLinLD + (lane & 7) * 16] = v[i];
+                __builtin_amdgcn_wave_barrier();
+                const i32x8 f = lin_join(*(const u32x4*)&lds[m * kLinLD + q * 16], *(const u32x4*)&lds[m * kLinLD + 64 + q * 16]);
+                __builtin_amdgcn_wave_barrier();
+                return f;
+            };
+            i32x8 fb[kG];
+#pragma unroll
+            for (int g = 0; g < kG; ++g) fb[g] = turn(bw[d][g]);
 #pragma unroll
             for (int t = 0; t < MT; ++t) {
-                const f32x4 p = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-                    lin_join(ax[d][t][0], ax[d][t][1]), fb, f32x4{0.f, 0.f, 0.f, 0.f}, 0, 0, 0,
-                    (int)sE[16 * t + m][kb] + 127, 0, kLinE8M0One);
+                const i32x8 fa = turn(ax[d][t]);
+                const int e = (int)sE[16 * t + m][kb] + 127;
 #pragma unroll
-                for (int r = 0; r < 4; ++r) acc[t][r] = fmaf(p[r], sc[d], acc[t][r]);
-                asm volatile("" : "+v"(acc[t]));  // (taken before the slot is loaded again)
+                for (int g = 0; g < kG; ++g) {
+                    const f32x4 p = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+                        fa, fb[g], f32x4{0.f, 0.f, 0.f, 0.f}, 0, 0, 0, e, 0, kLinE8M0One);
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) acc[t][g][r] = fmaf(p[r], sc[d], acc[t][g][r]);
+                }
             }
-            __builtin_amdgcn_wave_barrier();
+#pragma unroll
+            for (int t = 0; t < MT; ++t)
+#pragma unroll
+                for (int g = 0; g < kG; ++g) asm volatile("" : "+v"(acc[t][g]));  // (taken before the slot is loaded again)
             __builtin_amdgcn_sched_barrier(0);
             issue(tag);
             __builtin_amdgcn_sched_barrier(0);
             ++kb;
         });
     }
-    // the waves' sums, in wave order: wave t finishes row tile t
+    // the waves' sums, in wave order, a row tile at a time: wave g finishes column group g
 #pragma unroll
-    for (int t = 0; t < MT; ++t) red[wave][t][lane] = acc[t];
-    __syncthreads();
-    if (wave < MT) {
-        f32x4 v = red[0][wave][lane];
+    for (int t = 0; t < MT; ++t) {
+        if (t > 0) __syncthreads();
 #pragma unroll
-        for (int w = 1; w < kLinWaves; ++w) v += red[w][wave][lane];
-        const int n = n0 + m;
+        for (int g = 0; g < kG; ++g) red[wave][g][lane] = acc[t][g];
+        __syncthreads();
+        if (wave < kG) {
+            f32x4 v = red[0][wave][lane];
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            const int row = m0 + 16 * wave + 4 * q + r;
-            if (row < a.M && n < a.N) a.y[(size_t)row * a.N + n] = f32_to_bf16(v[r]);
+            for (int w = 1; w < kLinWaves; ++w) v += red[w][wave][lane];
+            const int n = n0 + 16 * wave + m;
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const int row = m0 + 16 * t + 4 * q + r;
+                if (row < a.M && n < a.N) a.y[(size_t)row * a.N + n] = f32_to_bf16(v[r]);
+            }
         }
     }
 }
@@ -329,8 +366,6 @@ __global__ __launch_bounds__(kWM * kWN * 64) void linear_tile_kernel(LinArgs a) 
         }
 }
 
-constexpr int kLinStreamM = 256;  // most rows of the streaming kernel
-
 template <typename F>
 static moe_status lin_launch(LinArgs a, int BM, int BN, int threads, F kernel, hipStream_t st) {
     a.m_tiles = (a.M + BM - 1) / BM;
@@ -357,9 +392,25 @@ extern "C" moe_status moe_linear_a8(const uint8_t* x_codes, const int8_t* x_exps
         return MOE_ERR_INVALID_ARG;
     LinArgs a{x_codes, x_exps, exp_pitch, M, N, K, w, s_w, y, 0, 0};
     hipStream_t st = as_stream(stream);
-    if (M <= 16) return lin_launch(a, 16, 16, kLinWaves * 64, linear_stream_kernel<1>, st);
-    if (M <= 32) return lin_launch(a, 32, 16, kLinWaves * 64, linear_stream_kernel<2>, st);
-    if (M <= kLinStreamM) return lin_launch(a, 64, 16, kLinWaves * 64, linear_stream_kernel<4>, st);
+    // Streaming or tiles, by the time each would take: the streaming kernel reads MT + kG tiles of 16 rows
+    // for every MT x kG of them (at the 7 TB/s that its loads come from the caches with), the tiles take
+    // 0.75 us a K step and round of 512 small ones.  Up to 64 rows always stream (the weights pass once).
+    const int MT = M <= 16 ? 1 : M <= 32 ? 2 : 4;
+    const int64_t rows = ((int64_t)M + 16 * MT - 1) / (16 * MT);
+    const int64_t cols = ((int64_t)N + 15) / 16;
+    // as many column groups a workgroup as leave one for most CUs
+    const int kG = rows * ((cols + 3) / 4) >= 192 ? 4 : rows * ((cols + 1) / 2) >= 192 ? 2 : 1;
+    const double stream_us = (double)rows * ((cols + kG - 1) / kG) * (MT + kG) * 16 * K / 7e6;
+    const int64_t small = ((int64_t)(M + 127) / 128) * ((N + 127) / 128);
+    const double tile_us = 0.75 * (K / 128) * ((small + 511) / 512);
+    if (M <= 64 || (M <= 1024 && stream_us < tile_us)) {
+#define MOE_STREAM(T_, G_) \
+    if (MT == T_ && kG == G_) return lin_launch(a, 16 * T_, 16 * G_, kLinWaves * 64, linear_stream_kernel<T_, G_>, st);
+        MOE_STREAM(1, 1) MOE_STREAM(1, 2) MOE_STREAM(1, 4)
+        MOE_STREAM(2, 1) MOE_STREAM(2, 2) MOE_STREAM(2, 4)
+        MOE_STREAM(4, 1) MOE_STREAM(4, 2) MOE_STREAM(4, 4)
+#undef MOE_STREAM
+    }
     const int64_t large = ((int64_t)(M + 255) / 256) * ((N + 255) / 256);
     if (large >= 192) return lin_launch(a, 256, 256, 512, linear_tile_kernel<4, 2, 4>, st);
     return lin_launch(a, 128, 128, 256, linear_tile_kernel<2, 2, 2>, st);
