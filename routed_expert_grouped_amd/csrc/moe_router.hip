@@ -11,7 +11,7 @@
 //   more        tiles on the matrix cores (32x32x16 bf16), operands through LDS.  When the tiles alone
 //               do not fill the chip, K is split over workgroups into fp32 partial scores in the
 //               caller's workspace, and a second launch adds them in order.  Up to a few thousand tokens
-//               64 x 64 tiles staged through registers; above, 128 x 256 or 128 x 128 tiles loaded directly
+//               64 x 64 tiles staged through registers; above, tiles of 128 x 256, 192 or 128 loaded directly
 //               to LDS, three stages deep.
 //
 // fp32 W goes to the matrix cores as three bf16 parts, w = hi + mid + lo (8 + 8 + 8 significand bits:
@@ -248,9 +248,16 @@ __device__ const u32x4 kRouterZeros = {0u, 0u, 0u, 0u};
 // 128 x (32 kNI kWN) tile, eight waves, K in stages of 64 and (fp32 W) of one of its planes, the small
 // parts first: stage s is K step s / planes.  Operand rows are 128 bytes in LDS, eight 16-byte chunks, chunk
 // c at slot c ^ ((row >> 1) & 7), so that 16 consecutive rows' reads of one chunk fall in distinct banks.
-// Loads go directly to LDS, two stages ahead in three buffers, 2 + kNI kWN / 2 a wave and stage; a stage
-// waits until only the next one's are in flight.  Rows past the end read the last row (not stored), chunks
-// past H read zeros.
+//
+// Loads go directly to LDS, three buffers.  A stage is four products' depths; each depth's fragments are read
+// while the one before is multiplied.  The stage's barrier stands before its last depth: every wave then
+// has all of the stage in registers, the next stage has landed (the one after it may be in flight: the
+// wait's count), and the freed buffer takes the stage after those.  The loop has no branch: past the end the
+// first stages are loaded again, into buffers that are not read.  Neighbouring workgroups of an XCD start one
+// K step apart and go round: rows of a whole number of 2 KiB have all of one step's lines in the same
+// memory channel (32768 x 7168 x 256: 144 us, all from the first step 149).
+// Rows past the end read the last row (not stored).  A last step of fewer than 64 values follows the loop,
+// with zeros for the chunks past H.
 template <int kMI, int kNI, int kWM, int kWN>
 __global__ __launch_bounds__(512) void router_dma_kernel(const uint16_t* __restrict__ x, int T, int H,
                                                          const uint16_t* __restrict__ w, int planes, int E,
@@ -264,50 +271,39 @@ __global__ __launch_bounds__(512) void router_dma_kernel(const uint16_t* __restr
     const int L = ((int)blockIdx.x & 7) * R8 + ((int)blockIdx.x >> 3);
     if (L >= tiles * splits) return;
     const int split = L / tiles, tile = L - split * tiles;
-    const int m0 = tile / n_tiles * kM, n0 = tile % n_tiles * kN;
-    const int steps = (H + kRtK - 1) / kRtK * planes;
-    const int k0 = (int)((int64_t)steps * split / splits), k1 = (int)((int64_t)steps * (split + 1) / splits);
+    const int m0 = uniform(tile / n_tiles * kM), n0 = uniform(tile % n_tiles * kN);
+    const int stages = H / kRtK * planes;  // (of whole steps)
+    const int k0 = (int)((int64_t)stages * split / splits), k1 = (int)((int64_t)stages * (split + 1) / splits);
 
     const int lane = lane_id(), wave = uniform((int)threadIdx.x >> 6);
     const int wm = wave / kWN, wn = wave % kWN, fr = lane & 31, half = lane >> 5;
-    const char *ap[kIA], *bp[kIB];
-    int ac[kIA], bc[kIB];  // the chunks this lane loads
+    uint32_t ao[kIA], bo[kIB];  // byte offsets from the tile's first row
+    const int chunk = (lane & 7) ^ ((lane >> 4) & 3);  // (rows 8 i + lane / 8: the swizzle's third bit is i's)
 #pragma unroll
-    for (int i = 0; i < kIA; ++i) {
-        const int r = 8 * (kIA * wave + i) + (lane >> 3);
-        ac[i] = (lane & 7) ^ ((r >> 1) & 7);
-        ap[i] = (const char*)(x + (size_t)min(m0 + r, T - 1) * H + 8 * ac[i]);
-    }
+    for (int i = 0; i < kIA; ++i)
+        ao[i] = (uint32_t)(min(8 * (kIA * wave + i) + (lane >> 3), T - 1 - m0) * H) * 2 +
+                16 * (chunk ^ (4 * ((kIA * wave + i) & 1)));
 #pragma unroll
-    for (int i = 0; i < kIB; ++i) {
-        const int r = 8 * (kIB * wave + i) + (lane >> 3);
-        bc[i] = (lane & 7) ^ ((r >> 1) & 7);
-        bp[i] = (const char*)(w + (size_t)min(n0 + r, E - 1) * H + 8 * bc[i]);
-    }
+    for (int i = 0; i < kIB; ++i)
+        bo[i] = (uint32_t)(min(8 * (kIB * wave + i) + (lane >> 3), E - 1 - n0) * H) * 2 +
+                16 * (chunk ^ (4 * ((kIB * wave + i) & 1)));
+    const char *xb = (const char*)(x + (size_t)m0 * H), *wb = (const char*)(w + (size_t)n0 * H);
     const size_t plane_bytes = (size_t)E * H * 2;
-    int step = k0 / planes, plane = planes - 1 - k0 % planes;  // of the next stage to load
-    const uint32_t la = lds_address(sA), lb = lds_address(sB);
-    auto issue = [&](int buf) {
-        const size_t at = (size_t)step * 128, bt = at + plane * plane_bytes;
-        const int left = H / 8 - 8 * step;  // chunks of this step
-        if (left >= 8) {
+    const uint32_t la = lds_address(sA) + 1024 * kIA * wave, lb = lds_address(sB) + 1024 * kIB * wave;
+    const int n_stages = k1 - k0;
+    int next = n_stages > 0 ? k0 + ((int)(blockIdx.x >> 3) * planes) % n_stages : 0;  // the next stage to load
+    size_t at = (size_t)(next / planes) * 128;
+    int plane = planes - 1 - next % planes;
+    auto issue = [&](uint32_t buf) {
+        const char *a = xb + at, *b = wb + at + plane * plane_bytes;
 #pragma unroll
-            for (int i = 0; i < kIA; ++i) lds_dma16_at(ap[i] + at, la + (buf * kM + 8 * (kIA * wave + i)) * 128);
+        for (int i = 0; i < kIA; ++i) lds_dma16_from(a, ao[i], la + buf * (kM * 128) + 1024 * i);
 #pragma unroll
-            for (int i = 0; i < kIB; ++i) lds_dma16_at(bp[i] + bt, lb + (buf * kN + 8 * (kIB * wave + i)) * 128);
-        } else {
-            const char* zeros = (const char*)&kRouterZeros;
-#pragma unroll
-            for (int i = 0; i < kIA; ++i)
-                lds_dma16_at(ac[i] < left ? ap[i] + at : zeros, la + (buf * kM + 8 * (kIA * wave + i)) * 128);
-#pragma unroll
-            for (int i = 0; i < kIB; ++i)
-                lds_dma16_at(bc[i] < left ? bp[i] + bt : zeros, lb + (buf * kN + 8 * (kIB * wave + i)) * 128);
-        }
-        if (--plane < 0) {
-            plane = planes - 1;
-            ++step;
-        }
+        for (int i = 0; i < kIB; ++i) lds_dma16_from(b, bo[i], lb + buf * (kN * 128) + 1024 * i);
+        const bool again = next + 1 == k1, wrap = plane == 0;
+        next = again ? k0 : next + 1;
+        at = again ? (size_t)(k0 / planes) * 128 : wrap ? at + 128 : at;
+        plane = again ? planes - 1 - k0 % planes : wrap ? planes - 1 : plane - 1;
     };
     f32x16 acc[kMI][kNI];
 #pragma unroll
@@ -316,31 +312,76 @@ __global__ __launch_bounds__(512) void router_dma_kernel(const uint16_t* __restr
         for (int j = 0; j < kNI; ++j)
 #pragma unroll
             for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.0f;
-    auto frag = [&](const uint8_t* t, int row, int c) {
-        return as_bf16x8(*(const u32x4*)&t[row * 128 + ((c ^ ((row >> 1) & 7)) << 4)]);
+    bf16x8 fa[2][kMI], fb[2][kNI];
+    const uint32_t sw = (fr >> 1) & 7;
+    auto read = [&](int set, uint32_t buf, int ks) {  // depth ks: chunk 2 ks + half
+        const uint32_t c = ((2 * ks + half) ^ sw) << 4;
+#pragma unroll
+        for (int i = 0; i < kMI; ++i) fa[set][i] = as_bf16x8(*(const u32x4*)&sA[buf][((wm * kMI + i) * 32 + fr) * 128 + c]);
+#pragma unroll
+        for (int j = 0; j < kNI; ++j) fb[set][j] = as_bf16x8(*(const u32x4*)&sB[buf][((wn * kNI + j) * 32 + fr) * 128 + c]);
     };
-    issue(0);
-    if (k0 + 1 < k1) issue(1);
-    int buf = 0;
-    for (int s = k0; s < k1; ++s) {
-        if (s + 1 < k1) __builtin_amdgcn_s_waitcnt(vmcnt_imm(kIA + kIB));
-        else __builtin_amdgcn_s_waitcnt(vmcnt_imm(0));
-        __syncthreads();  // stage s is in LDS, and every wave has left stage s - 1's buffer
-        if (s + 2 < k1) issue(buf == 0 ? 2 : buf - 1);
+    auto multiply = [&](int set) {
 #pragma unroll
-        for (int ks = 0; ks < kRtK / 16; ++ks) {
-            bf16x8 fa[kMI], fb[kNI];
+        for (int i = 0; i < kMI; ++i)
 #pragma unroll
-            for (int i = 0; i < kMI; ++i) fa[i] = frag(sA[buf], (wm * kMI + i) * 32 + fr, 2 * ks + half);
-#pragma unroll
-            for (int j = 0; j < kNI; ++j) fb[j] = frag(sB[buf], (wn * kNI + j) * 32 + fr, 2 * ks + half);
-#pragma unroll
-            for (int i = 0; i < kMI; ++i)
-#pragma unroll
-                for (int j = 0; j < kNI; ++j)
-                    acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fa[i], fb[j], acc[i][j], 0, 0, 0);
+            for (int j = 0; j < kNI; ++j)
+                acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fa[set][i], fb[set][j], acc[i][j], 0, 0, 0);
+    };
+    if (k0 < k1) {
+        issue(0);
+        issue(1);
+        issue(2);
+        __builtin_amdgcn_s_waitcnt(vmcnt_imm(2 * (kIA + kIB)));
+        __syncthreads();
+        read(0, 0, 0);
+        uint32_t buf = 0;
+        for (int s = k0; s < k1; ++s) {
+            const uint32_t after = buf == 2 ? 0 : buf + 1;
+            read(1, buf, 1);
+            __builtin_amdgcn_sched_barrier(0);
+            multiply(0);
+            __builtin_amdgcn_sched_barrier(0);
+            read(0, buf, 2);
+            __builtin_amdgcn_sched_barrier(0);
+            multiply(1);
+            __builtin_amdgcn_sched_barrier(0);
+            read(1, buf, 3);
+            __builtin_amdgcn_sched_barrier(0);
+            multiply(0);
+            __builtin_amdgcn_sched_barrier(0);
+            __builtin_amdgcn_s_waitcnt(vmcnt_imm(kIA + kIB));
+            __syncthreads();
+            read(0, after, 0);  // (after the last stage: not used)
+            issue(buf);
+            __builtin_amdgcn_sched_barrier(0);
+            multiply(1);
+            __builtin_amdgcn_sched_barrier(0);
+            buf = after;
         }
-        buf = buf == 2 ? 0 : buf + 1;
+        __builtin_amdgcn_s_waitcnt(vmcnt_imm(0));
+    }
+    if (H % kRtK != 0 && split == splits - 1) {
+        const int left = H % kRtK / 8;  // chunks of the last step
+        for (int p = planes - 1; p >= 0; --p) {
+            __syncthreads();  // every wave has left the buffer
+            const char *a = xb + (size_t)(H / kRtK) * 128, *b = wb + (size_t)(H / kRtK) * 128 + p * plane_bytes;
+#pragma unroll
+            for (int i = 0; i < kIA; ++i)
+                lds_dma16_at((chunk ^ (4 * ((kIA * wave + i) & 1))) < left ? a + ao[i] : (const char*)&kRouterZeros,
+                             la + 1024 * i);
+#pragma unroll
+            for (int i = 0; i < kIB; ++i)
+                lds_dma16_at((chunk ^ (4 * ((kIB * wave + i) & 1))) < left ? b + bo[i] : (const char*)&kRouterZeros,
+                             lb + 1024 * i);
+            __builtin_amdgcn_s_waitcnt(vmcnt_imm(0));
+            __syncthreads();
+#pragma unroll
+            for (int ks = 0; ks < 4; ++ks) {
+                read(0, 0, ks);
+                multiply(0);
+            }
+        }
     }
     float* o = out + (size_t)split * T * E;
 #pragma unroll
@@ -388,8 +429,16 @@ static RouterPlan router_plan(int T, int H, int E, bool f32) {
     RouterPlan p{};
     p.dma = T >= kRouterDmaT;
     p.kM = p.dma ? 128 : 64;
-    // 256 columns, or 128 where the last 256 would be half empty
-    p.kN = !p.dma ? 64 : (E + 127) / 128 % 2 == 0 ? 256 : 128;
+    // of 256, 192 and 128 columns the width that loads the fewest rows, kN of W and 128 of x a tile
+    // (32768 x 7168 x 384: 192 columns 203 us, 128 columns 229)
+    p.kN = 64;
+    if (p.dma) {
+        int best = INT32_MAX;
+        for (int kN : {256, 192, 128}) {
+            const int rows = (E + kN - 1) / kN * (kN + 128);
+            if (rows < best) best = rows, p.kN = kN;
+        }
+    }
     p.n_tiles = (E + p.kN - 1) / p.kN;
     p.tiles = (T + p.kM - 1) / p.kM * p.n_tiles;
     // one round of workgroups (two a CU of the small tiles), at least four K steps each
@@ -467,6 +516,8 @@ extern "C" moe_status moe_router_scores(const uint16_t* x, int32_t T, int32_t H,
         const int planes = f32 ? 3 : 1;
         if (p.kN == 256)
             router_dma_kernel<2, 2, 2, 4><<<grid, dim3(512), 0, st>>>(x, T, H, wb, planes, E, p.n_tiles, p.tiles, splits, o);
+        else if (p.kN == 192)
+            router_dma_kernel<1, 3, 4, 2><<<grid, dim3(512), 0, st>>>(x, T, H, wb, planes, E, p.n_tiles, p.tiles, splits, o);
         else
             router_dma_kernel<1, 2, 4, 2><<<grid, dim3(512), 0, st>>>(x, T, H, wb, planes, E, p.n_tiles, p.tiles, splits, o);
     } else if (f32) {

@@ -17,6 +17,9 @@ SIZES = [  # T, H, E: both kernels, ragged tiles, K tails, split and unsplit
     (1, 8, 1), (1, 7168, 256), (2, 256, 7), (3, 520, 16), (4, 1024, 64), (5, 2048, 129), (8, 7168, 384),
     (9, 264, 33), (16, 7168, 256), (17, 7168, 256), (31, 8, 5), (64, 72, 130), (127, 512, 128),
     (128, 1032, 129), (129, 2048, 255), (333, 7168, 384), (1000, 640, 1024), (4096, 512, 256),
+    # the large batches' tiles: one and several K steps, none that is whole, a last one of one chunk, both widths
+    (2048, 64, 256), (2049, 8, 5), (2047, 72, 130), (2048, 72, 130), (2100, 1032, 384), (2300, 120, 300),
+    (2048, 7168, 256), (2177, 2056, 1000), (5000, 192, 256), (2200, 1160, 100), (2050, 4096, 192),
 ]
 
 
@@ -50,7 +53,7 @@ def test_whole_numbers_are_exact(T, H, E, f32):
     assert torch.equal(got, x.double() @ w.double().T)
 
 
-@pytest.mark.parametrize("T", [1, 5, 16, 17, 300])
+@pytest.mark.parametrize("T", [1, 5, 16, 17, 300, 2500])
 def test_every_bit_of_an_fp32_weight_counts(T):
     """Rows that pick one weight each return it bit for bit."""
     H, E = 256, 40
@@ -62,7 +65,7 @@ def test_every_bit_of_an_fp32_weight_counts(T):
     assert torch.equal(call(bits(x), w, T, E), w[:, pick].T.double())
 
 
-@pytest.mark.parametrize("T", [4, 16, 40])
+@pytest.mark.parametrize("T", [4, 16, 40, 2100])
 def test_nan_and_infinity_stay_in_their_row_or_column(T):
     H, E = 328, 48
     gen = rng(T)
@@ -107,7 +110,7 @@ def test_no_tokens():
     assert moe.moe_router_scores(x, w).shape == (0, 8)
 
 
-@pytest.mark.parametrize("T", [3, 200])
+@pytest.mark.parametrize("T", [3, 200, 2048])
 def test_streams_and_graph(T):
     gen = rng(T)
     x, w = bits(randn(gen, T, 2048)).to(DEV), bits(randn(gen, 256, 2048)).to(DEV)
