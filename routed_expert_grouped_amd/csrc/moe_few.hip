@@ -41,7 +41,8 @@ namespace moe {
 constexpr int kFewT = MOE_FEW_MAX_TOKENS;
 constexpr int kFewWaves = 8;
 constexpr int kFewThreads = kFewWaves * kWave;
-constexpr int kFewXBytes = 114816;   // LDS for x: 8 rows of 7168 bf16, padded by 16 bytes each
+constexpr int kFewXBytes = 114816;   // LDS for x: 8 rows of 7168 bf16, padded by 16 bytes each ...
+constexpr int kFewCodeBytes = kFewXBytes + 16 * kFewT;  // ... or 16 of codes, as many more
 constexpr int kFewList = kFewT * MOE_MAX_TOPK;  // most touched experts
 constexpr int kFewShared = 0xFFFF;   // the shared expert's id in the list
 constexpr size_t kFewHead = 2048;    // workspace: list (count, then id | token mask << 16), then h
@@ -157,6 +158,80 @@ __device__ __forceinline__ void few_stage(uint8_t* lds, const u32x4 (*w)[2], int
     }
 }
 
+typedef int i32x8 __attribute__((__vector_size__(8 * sizeof(int))));
+constexpr int kFewFP8Codes = 0, kFewFP4Codes = 4;  // the scaled instruction's operand formats
+
+// Eight bf16 values of x (16 consecutive lanes have a 128-block) as two E4M3 values each, x = 2^e hi +
+// 2^(e - 4) lo: hi holds the first four significand bits, and what is left is at most half of hi's last
+// place, 16 2^e, with four significand bits: lo holds it exactly.  Only where hi is subnormal (below 2^-14 of
+// the block's largest, which is over 224 2^e) may lo lose bits, at most 2^-14 2^e: less than 2^-21 of
+// the block's largest value.  Returns e (>= -123, so that e - 4 is an E8M0 scale too).
+__device__ __forceinline__ int few_codes(u32x4 v, uint2& hi, uint2& lo) {
+    float f[8];
+    float amax = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        f[2 * i] = __uint_as_float(v[i] << 16);
+        f[2 * i + 1] = __uint_as_float(v[i] & 0xffff0000u);
+        amax = fmaxf(amax, fmaxf(fabsf(f[2 * i]), fabsf(f[2 * i + 1])));  // (a NaN takes no part)
+    }
+    amax = __uint_as_float(row16_max_u32(__float_as_uint(amax)));
+    const int e = isinf(amax) ? 127 : max(-123, act_scale_exp(amax));
+    uint32_t h[2], l[2];
+#pragma unroll
+    for (int w = 0; w < 2; ++w) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) f[4 * w + i] = ldexpf(f[4 * w + i], -e);
+        int c = __builtin_amdgcn_cvt_pk_fp8_f32(f[4 * w], f[4 * w + 1], 0, false);
+        c = __builtin_amdgcn_cvt_pk_fp8_f32(f[4 * w + 2], f[4 * w + 3], c, true);
+        const auto a = __builtin_amdgcn_cvt_pk_f32_fp8(c, false), b = __builtin_amdgcn_cvt_pk_f32_fp8(c, true);
+        h[w] = (uint32_t)c;
+        c = __builtin_amdgcn_cvt_pk_fp8_f32(16.0f * (f[4 * w] - a[0]), 16.0f * (f[4 * w + 1] - a[1]), 0, false);
+        l[w] = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(16.0f * (f[4 * w + 2] - b[0]), 16.0f * (f[4 * w + 3] - b[1]), c, true);
+    }
+    hi = make_uint2(h[0], h[1]);
+    lo = make_uint2(l[0], l[1]);
+    return e;
+}
+
+// An MXFP4 stage of kG times 16 weight rows times x in codes (few_codes): the scaled 16x16x128
+// instruction takes both operands' codes and scales as they are, a block each.  Its 4-bit operand has 32
+// consecutive values in a lane quarter, kq's block of scale group kq; the 8-bit one 16 from 16 kq and 16 from
+// 64 + 16 kq.  se: the E8M0 scales of this lane's row of x, blocks 0 and 1 in bytes 0 and 1.
+template <int kG>
+__device__ __forceinline__ void few_stage_codes(uint8_t* lds, const u32x4 (*w)[2], int lane, uint32_t sv, int se,
+                                                const i32x8 (&x)[2], f32x4 (*acc)[2]) {
+    const int m = lane & 15, kq = lane >> 4;
+    const uint8_t* row = lds + m * kFewLD;
+    u32x4 v[kG][2];
+#pragma unroll
+    for (int g = 0; g < kG; ++g) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) *(u32x4*)&lds[(8 * i + (lane >> 3)) * kFewLD + (lane & 7) * 16] = w[g][i];
+        __builtin_amdgcn_wave_barrier();
+#pragma unroll
+        for (int i = 0; i < 2; ++i) v[g][i] = *(const u32x4*)&row[64 * i + 16 * kq];
+        __builtin_amdgcn_wave_barrier();
+    }
+    int f[kG][2];
+#pragma unroll
+    for (int g = 0; g < kG; ++g)
+#pragma unroll
+        for (int b = 0; b < 2; ++b)
+            f[g][b] = (int)((uint32_t)__builtin_amdgcn_ds_bpermute(4 * (2 * (16 * g + m) + b), (int)sv) >> (8 * kq));
+#pragma unroll
+    for (int g = 0; g < kG; ++g) {
+        const i32x8 w0 = {(int)v[g][0][0], (int)v[g][0][1], (int)v[g][0][2], (int)v[g][0][3], 0, 0, 0, 0};
+        const i32x8 w1 = {(int)v[g][1][0], (int)v[g][1][1], (int)v[g][1][2], (int)v[g][1][3], 0, 0, 0, 0};
+        acc[g][0] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(x[0], w0, acc[g][0], kFewFP8Codes, kFewFP4Codes,
+                                                                    0, se, 0, f[g][0]);
+        acc[g][1] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(x[1], w1, acc[g][1], kFewFP8Codes, kFewFP4Codes,
+                                                                    1, se, 0, f[g][1]);
+    }
+#pragma unroll
+    for (int g = 0; g < kG; ++g) asm volatile("" : "+v"(acc[g][0]), "+v"(acc[g][1]));  // (as in few_stage)
+}
+
 template <int kG>
 __device__ __forceinline__ void few_clear(f32x4 (*acc)[2]) {
 #pragma unroll
@@ -173,8 +248,10 @@ template <int kFmt, int kG>
 __global__ __launch_bounds__(kFewThreads) void few_gate_up_kernel(FewArgs a) {
     using F = FewFmt<kFmt>;
     constexpr int D = kFewRing, kCols = 8 * kG;
-    __shared__ __attribute__((aligned(16))) uint8_t sX[kFewXBytes];
-    __shared__ __attribute__((aligned(16))) uint8_t sZero[64];
+    constexpr bool kCodes = kFmt == kFewMX;  // x in LDS: E4M3 codes (rows t hi, T + t lo), else bf16
+    __shared__ __attribute__((aligned(16))) uint8_t sX[kCodes ? kFewCodeBytes : kFewXBytes];
+    __shared__ __attribute__((aligned(16))) uint8_t sE[kCodes ? kFewCodeBytes / 128 + 2 * kFewT : 2];  // the codes' E8M0 scales
+    __shared__ __attribute__((aligned(16))) uint8_t sZero[128];
     __shared__ __attribute__((aligned(16))) uint8_t sW[kFewWaves][16 * kFewLD];
     __shared__ float red[2][kFewWaves][kG][32 * 4];
     __shared__ int32_t sids[kFewList];
@@ -254,11 +331,25 @@ __global__ __launch_bounds__(kFewThreads) void few_gate_up_kernel(FewArgs a) {
         });
     }
     // ---- x into LDS, rows padded by 16 bytes (row m starts 4 m banks on)
-    const int xrow = 2 * H + 16, chunks = H / 8;
-    if (tid < 4) *(u32x4*)&sZero[16 * tid] = u32x4{0u, 0u, 0u, 0u};
+    const int xrow = (kCodes ? H : 2 * H) + 16, chunks = H / 8, epitch = (kb_all + 1) & ~1;
+    if (tid < 8) *(u32x4*)&sZero[16 * tid] = u32x4{0u, 0u, 0u, 0u};
     for (int c = tid; c < T * chunks; c += kFewThreads) {
         const int t = c / chunks, j = c - t * chunks;
-        *(u32x4*)&sX[t * xrow + 16 * j] = ((const u32x4*)(a.x + (size_t)t * H))[j];
+        const u32x4 v = ((const u32x4*)(a.x + (size_t)t * H))[j];
+        if (kCodes) {  // (chunks is a multiple of 16: a block's 16 lanes are in the loop together)
+            uint2 hi, lo;
+            const int e = few_codes(v, hi, lo);
+            *(uint2*)&sX[t * xrow + 8 * j] = hi;
+            *(uint2*)&sX[(T + t) * xrow + 8 * j] = lo;
+            if ((j & 15) == 0) {
+                const int b = j / 16;
+                sE[t * epitch + b] = (uint8_t)(127 + e);
+                sE[(T + t) * epitch + b] = (uint8_t)(123 + e);
+                if (b + 1 == kb_all && b + 1 < epitch) sE[t * epitch + b + 1] = sE[(T + t) * epitch + b + 1] = 127;
+            }
+        } else {
+            *(u32x4*)&sX[t * xrow + 16 * j] = v;
+        }
     }
     // ---- routing: token t by wave t
     if (tid < MOE_MAX_EXPERTS / 32) bits[tid] = 0u;
@@ -321,18 +412,32 @@ __global__ __launch_bounds__(kFewThreads) void few_gate_up_kernel(FewArgs a) {
     }
 
     // this lane's x row, at its quarter; rows past the last token repeat token 0 (not stored)
-    const uint8_t* xm = sX + (m < T ? m : 0) * xrow + 2 * F::value(0, kq);
+    // (codes: rows 8 + t are the lo codes)
+    const int xr = kCodes ? ((m & 7) < T ? (m & 7) : 0) + (m < 8 ? 0 : T) : m < T ? m : 0;
+    const uint8_t* xm = sX + xr * xrow + (kCodes ? 16 * kq : 2 * F::value(0, kq));
+    const uint8_t* em = sE + xr * epitch;
     f32x4 acc[kG][2];
     few_clear<kG>(acc);
     auto compute = [&](auto tag, int st) {
         constexpr int d = decltype(tag)::value;
-        const uint8_t* x0 = xm + 2 * st * F::kSV;
-        const uint8_t* x1 = kFmt == kFewMX && 2 * st + 1 >= kb_all ? sZero : x0 + 256;  // MXFP4's second block
-        bf16x8 xv[F::kNM];
+        if constexpr (kCodes) {
+            const uint8_t* x0 = xm + st * F::kSV;
+            const uint8_t* x1 = 2 * st + 1 >= kb_all ? sZero : x0 + 128;  // the second block
+            i32x8 xv[2];
 #pragma unroll
-        for (int i = 0; i < F::kNM; ++i) xv[i] = as_bf16x8(*(const u32x4*)&(i < 4 ? x0 : x1)[16 * (i & 3)]);
-        few_stage<kFmt, kG>(lds, bw[d], lane, kFmt == kFewMX ? mx[d] : 0u, kFmt == kFewFP8 ? sc[d] : 0.0f,
-                            [&](int i) { return xv[i]; }, acc);
+            for (int b = 0; b < 2; ++b) {
+                const u32x4 p = *(const u32x4*)(b ? x1 : x0), q = *(const u32x4*)((b ? x1 : x0) + 64);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) xv[b][i] = (int)p[i], xv[b][4 + i] = (int)q[i];
+            }
+            few_stage_codes<kG>(lds, bw[d], lane, mx[d], *(const uint16_t*)(em + 2 * st), xv, acc);
+        } else {
+            const uint8_t* x0 = xm + 2 * st * F::kSV;
+            bf16x8 xv[F::kNM];
+#pragma unroll
+            for (int i = 0; i < F::kNM; ++i) xv[i] = as_bf16x8(*(const u32x4*)&x0[16 * i]);
+            few_stage<kFmt, kG>(lds, bw[d], lane, 0u, kFmt == kFewFP8 ? sc[d] : 0.0f, [&](int i) { return xv[i]; }, acc);
+        }
     };
     int cu = (int)blockIdx.x, seq = 0;  // the unit being computed
     // Joins the waves' sums of the unit; kG of the waves, in turn, then finish its columns: wave
@@ -340,8 +445,13 @@ __global__ __launch_bounds__(kFewThreads) void few_gate_up_kernel(FewArgs a) {
     auto finish = [&]() {
 #pragma unroll
         for (int g = 0; g < kG; ++g) {
-            // tokens 0..7 are rows 0..7: lanes 0..31
-            if (lane < 32) *(f32x4*)&red[seq & 1][wave][g][4 * lane] = kFmt == kFewFP8 ? acc[g][0] : acc[g][0] + acc[g][1];
+            // tokens 0..7 are rows 0..7: lanes 0..31 (and rows 8..15 their lo parts: lanes 32..63)
+            f32x4 v = kFmt == kFewFP8 ? acc[g][0] : acc[g][0] + acc[g][1];
+            if (kCodes) {
+#pragma unroll
+                for (int r = 0; r < 4; ++r) v[r] += __shfl_xor(v[r], 32, kWave);
+            }
+            if (lane < 32) *(f32x4*)&red[seq & 1][wave][g][4 * lane] = v;
         }
         few_clear<kG>(acc);
         lds_barrier();

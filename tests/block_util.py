@@ -76,7 +76,7 @@ def expert64(ew, e, x):
 def layer64(layer, ids, wts):
     """(out, error bound) of a synth.Layer in float64 for the routing ids, wts [T, k].  The bound takes
     sums of n fp32 terms as off by n * 2^-23 * sum|terms| (any order, products of scaled blocks rounded
-    too), SiLU * up as 2^-18 (1 + |g|) relative (exp, its argument, and the reciprocal), w * h
+    too), with MXFP4 weights a value of x as off by 2^-21 of its 128-block's largest, SiLU * up as 2^-18 (1 + |g|) relative (exp, its argument, and the reciprocal), w * h
     kept in two bf16 values as 2^-15; bf16's half step of the output (2^-8) comes on top."""
     dev = layer.x.device
     x = layer.x.view(torch.bfloat16).double()
@@ -95,6 +95,10 @@ def layer64(layer, ids, wts):
         g, u, ag, au = expert64(ew, e, x[t])
         h = g * torch.sigmoid(g) * u
         dg, du = layer.H * 2.0 ** -23 * ag, layer.H * 2.0 ** -23 * au
+        if ew.wdtype == "mxfp4":
+            top = x[t].abs().unflatten(1, (-1, 128)).amax(2).repeat_interleave(128, 1)
+            more = expert64(ew, e, 2.0 ** -21 * top)
+            dg, du = dg + more[2], du + more[3]
         dh = 1.1 * (u.abs() + du) * dg + (g * torch.sigmoid(g)).abs() * du + h.abs() * (2.0 ** -15 + 2.0 ** -18 * (1 + g.abs()))
         wd = weights64(ew.wdtype, ew.down[e], None if ew.s_down is None else ew.s_down[e])
         out[t] += (w * h) @ wd.T

@@ -88,6 +88,25 @@ def test_full_size(wdtype, T):
     check(layer)
 
 
+@pytest.mark.parametrize("wdtype", ["fp8", "bf16", "mxfp4"])
+@pytest.mark.parametrize("T", [1, 5])
+def test_rows_of_a_wide_range(wdtype, T):
+    """Values from 2^-40 to 2^40 in one block, blocks of zeros, the smallest values of the type, and a sum that
+    only the small ones make."""
+    layer = make(T, 512, 256, 12, 3, wdtype, seed=40 + T)
+    gen = torch.Generator().manual_seed(T)
+    v = layer.x.cpu().view(torch.bfloat16).float()
+    v *= torch.exp2(torch.randint(-40, 41, v.shape, generator=gen).float())
+    v[:, 128:256] = 0.0
+    v[:, 256:384] = torch.randint(-3, 4, (T, 128), generator=gen) * 2.0 ** -133
+    v[0] = 0.0
+    v[0, 384:] = layer.x[0, 384:].cpu().view(torch.bfloat16).float() * 2.0 ** -100
+    layer.x.copy_(v.to(torch.bfloat16).view(torch.int16))
+    out, ids, wts = run(layer)
+    ref, tol = layer64(layer, ids.cpu(), wts.cpu())
+    assert bool(((out.view(torch.bfloat16).double() - ref).abs() <= ref.abs() * 2.0 ** -8 + (1 + 2.0 ** -8) * tol + 2.0 ** -126).all())
+
+
 def test_all_tokens_on_one_expert():
     layer = make(8, 512, 256, 12, 1, "fp8", seed=4)
     layer.scores.fill_(0.0)
