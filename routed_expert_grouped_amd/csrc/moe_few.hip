@@ -322,23 +322,51 @@ __global__ __launch_bounds__(kFewThreads) void few_gate_up_kernel(FewArgs a) {
         }
     };
 
-    // the shared expert's first stages, before anything is known of the routing
+    // ---- loads in the order they are needed in: the scores (token t by wave t), x, and the shared expert's
+    // first stages, which are in flight while the routing runs
+    float sv[MOE_MAX_EXPERTS / kWave];
+    if (wave < T) {
+#pragma unroll
+        for (int i = 0; i < MOE_MAX_EXPERTS / kWave; ++i)
+            if (kWave * i < a.E) {
+                const int e = lane + kWave * i;
+                sv[i] = e < a.E ? a.scores[(size_t)wave * a.E + e] : 0.0f;
+            }
+    }
+    constexpr int kX = (kFewXBytes / 16 + kFewThreads - 1) / kFewThreads;  // chunks of x a thread, at most
+    const int chunks = H / 8;
+    u32x4 xc[kX];
+#pragma unroll
+    for (int i = 0; i < kX; ++i)
+        if (kFewThreads * i < T * chunks) xc[i] = ((const u32x4*)a.x)[min(tid + kFewThreads * i, T * chunks - 1)];
+    __builtin_amdgcn_sched_barrier(0);
     const int pre = iu < n_units ? min(D, ns) : 0;
     if (pre > 0) {
         unit_of(iu);
         each_slot<D>([&](auto tag) {
-            if (decltype(tag)::value < pre) issue(tag);
+            issue(tag);
+            __builtin_amdgcn_sched_barrier(0);
         });
+        __builtin_amdgcn_s_waitcnt(vmcnt_imm(D * (2 * kG + (kFmt == kFewBF16 ? 0 : 1))));  // (all but the ring's)
+        if (pre == ns) {  // the cursor back to the unit's last stage: slots from `pre` on are loaded again below
+            iu = (int)blockIdx.x;
+            ib = ns - 1;
+        }
+    } else {
+        __builtin_amdgcn_s_waitcnt(vmcnt_imm(0));
     }
     // ---- x into LDS, rows padded by 16 bytes (row m starts 4 m banks on)
-    const int xrow = (kCodes ? H : 2 * H) + 16, chunks = H / 8, epitch = (kb_all + 1) & ~1;
+    const int xrow = (kCodes ? H : 2 * H) + 16, epitch = (kb_all + 1) & ~1;
+    const uint32_t inv = 0xFFFFFFFFu / (uint32_t)chunks + 1;  // c / chunks is the product's high half (c < 2^13)
     if (tid < 8) *(u32x4*)&sZero[16 * tid] = u32x4{0u, 0u, 0u, 0u};
-    for (int c = tid; c < T * chunks; c += kFewThreads) {
-        const int t = c / chunks, j = c - t * chunks;
-        const u32x4 v = ((const u32x4*)(a.x + (size_t)t * H))[j];
-        if (kCodes) {  // (chunks is a multiple of 16: a block's 16 lanes are in the loop together)
+#pragma unroll
+    for (int i = 0; i < kX; ++i) {
+        const int c = tid + kFewThreads * i;
+        if (c >= T * chunks) break;
+        const int t = (int)__umulhi((uint32_t)c, inv), j = c - t * chunks;
+        if (kCodes) {  // (chunks is a multiple of 16: a block's 16 lanes are here together)
             uint2 hi, lo;
-            const int e = few_codes(v, hi, lo);
+            const int e = few_codes(xc[i], hi, lo);
             *(uint2*)&sX[t * xrow + 8 * j] = hi;
             *(uint2*)&sX[(T + t) * xrow + 8 * j] = lo;
             if ((j & 15) == 0) {
@@ -348,21 +376,20 @@ __global__ __launch_bounds__(kFewThreads) void few_gate_up_kernel(FewArgs a) {
                 if (b + 1 == kb_all && b + 1 < epitch) sE[t * epitch + b + 1] = sE[(T + t) * epitch + b + 1] = 127;
             }
         } else {
-            *(u32x4*)&sX[t * xrow + 16 * j] = v;
+            *(u32x4*)&sX[t * xrow + 16 * j] = xc[i];
         }
     }
-    // ---- routing: token t by wave t
+    // ---- routing
     if (tid < MOE_MAX_EXPERTS / 32) bits[tid] = 0u;
     if (tid < kFewList) list[tid] = 0u;
     if (wave < T) {
-        const float* s = a.scores + (size_t)wave * a.E;
         int32_t* ri = sids + wave * k;
         float* rw = swts + wave * k;
-        if (a.E <= 64) route_token<1>(s, a.E, k, a.score_fn, a.renorm, ri, rw);
-        else if (a.E <= 128) route_token<2>(s, a.E, k, a.score_fn, a.renorm, ri, rw);
-        else if (a.E <= 256) route_token<4>(s, a.E, k, a.score_fn, a.renorm, ri, rw);
-        else if (a.E <= 512) route_token<8>(s, a.E, k, a.score_fn, a.renorm, ri, rw);
-        else route_token<16>(s, a.E, k, a.score_fn, a.renorm, ri, rw);
+        if (a.E <= 64) route_values<1>(sv, a.E, k, a.score_fn, a.renorm, ri, rw);
+        else if (a.E <= 128) route_values<2>(sv, a.E, k, a.score_fn, a.renorm, ri, rw);
+        else if (a.E <= 256) route_values<4>(sv, a.E, k, a.score_fn, a.renorm, ri, rw);
+        else if (a.E <= 512) route_values<8>(sv, a.E, k, a.score_fn, a.renorm, ri, rw);
+        else route_values<16>(sv, a.E, k, a.score_fn, a.renorm, ri, rw);
     }
     __syncthreads();
     if (tid < T * k) atomicOr(&bits[sids[tid] >> 5], 1u << (sids[tid] & 31));
@@ -398,7 +425,7 @@ __global__ __launch_bounds__(kFewThreads) void few_gate_up_kernel(FewArgs a) {
             iu = (int)blockIdx.x;
             ib = 0;
             unit_of(iu);
-        } else if (pre == ns && iu == (int)blockIdx.x && iu + grid < n_units) {
+        } else if (pre == ns && iu + grid < n_units) {
             // the whole shared unit is loaded, and its successor was not known yet
             iu += grid;
             ib = 0;

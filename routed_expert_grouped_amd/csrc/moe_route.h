@@ -62,21 +62,16 @@ __device__ __forceinline__ double wave_sum_f64(double x) {
     return ((lane_value(0) + lane_value(16)) + lane_value(32)) + lane_value(48);
 }
 
-// Routes one token: s = its E scores; writes ids[0..k) and w[0..k) (and the ids to lds_ids too,
-// when it is not null).  Must be called by a whole wave.
+// Routes one token: v = this lane's scores, of the experts lane + 64 i below E; writes ids[0..k) and w[0..k)
+// (and the ids to lds_ids too, when it is not null).  Must be called by a whole wave.
 template <int VPL>
-__device__ __forceinline__ void route_token(const float* __restrict__ s, int E, int k, int score_fn,
-                                            int renorm, int32_t* __restrict__ ids,
-                                            float* __restrict__ wts, int* lds_ids = nullptr) {
+__device__ __forceinline__ void route_values(const float* v, int E, int k, int score_fn, int renorm,
+                                             int32_t* __restrict__ ids, float* __restrict__ wts,
+                                             int* lds_ids = nullptr) {
     const int lane = lane_id();
-    float v[VPL];
     uint32_t key[VPL];
 #pragma unroll
-    for (int i = 0; i < VPL; ++i) {
-        const int e = lane + kWave * i;
-        v[i] = e < E ? s[e] : 0.0f;
-        key[i] = e < E ? score_key(v[i]) : 0u;
-    }
+    for (int i = 0; i < VPL; ++i) key[i] = lane + kWave * i < E ? score_key(v[i]) : 0u;
     int my_id = -1;
     float my_s = 0.0f;
     for (int j = 0; j < k; ++j) {
@@ -138,6 +133,20 @@ __device__ __forceinline__ void route_token(const float* __restrict__ s, int E, 
         wts[lane] = (float)(num / den);
         if (lds_ids) lds_ids[lane] = my_id;
     }
+}
+
+// The same from memory: s = the token's E scores.
+template <int VPL>
+__device__ __forceinline__ void route_token(const float* __restrict__ s, int E, int k, int score_fn,
+                                            int renorm, int32_t* __restrict__ ids,
+                                            float* __restrict__ wts, int* lds_ids = nullptr) {
+    float v[VPL];
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) {
+        const int e = lane_id() + kWave * i;
+        v[i] = e < E ? s[e] : 0.0f;
+    }
+    route_values<VPL>(v, E, k, score_fn, renorm, ids, wts, lds_ids);
 }
 
 // VPL (scores per lane) for E experts: the smallest of 1, 2, 4, 8, 16 with 64 * VPL >= E.
