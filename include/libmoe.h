@@ -399,9 +399,11 @@ moe_status moe_linear_a8(const uint8_t* x_codes, const int8_t* x_exps, int32_t e
  *              output (weight 1), 0 without one
  * Nothing between x and out is rounded to bf16: w_tj h_te is kept to 16 significand bits and every
  * sum in fp32, so the result is closer to the formula than the separate calls' (which round h and
- * y to bf16).  Sums run over the touched experts in ascending order, in parts that depend on the
- * sizes and the routing alone: equal inputs give equal bits.  Each touched expert's weights are
- * read once; a token's output depends on its own row and on the weights of its own experts.
+ * y to bf16).  With MXFP4 weights x goes to the matrix cores as two E4M3 values each, exact down to
+ * 2^-21 of the largest value in its 128-block.  Sums run over the touched experts in ascending order,
+ * in parts that depend on the sizes and the routing alone: equal inputs give equal bits.  Each touched
+ * expert's weights are read once; a token's output depends on its own row and on the weights of its
+ * own experts.
  *   scores : fp32 [T][E], finite, E = w->n_groups.     x : bf16 [T][H].
  *   shared : one expert (n_groups == 1, dtype, H and I as w) or NULL.
  *   topk_ids, topk_w : int32 [T][k], fp32 [T][k] out, bit for bit moe_route's.

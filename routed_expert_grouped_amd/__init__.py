@@ -499,6 +499,7 @@ def moe_linear_a8(codes, exps, w, s_w, y=None, stream=None):
 
 
 FEW_MAX_TOKENS = 8  # MOE_FEW_MAX_TOKENS
+FEW_MAX_X = 57408   # moe_layer_few's limit on T * (H + 8)
 
 
 def moe_layer_few_workspace_size(T: int, k: int, w: MoeExpertWeights) -> int:
@@ -572,13 +573,19 @@ class MoeLayer:
     act="fp8" selects the FP8 activation mode (moe_expert_ffn_a8) for the routed and the shared
     experts; `h` then views the routed h inside the workspace, before its quantisation.
 
+    few=True runs the layer as moe_layer_few: two launches, for up to FEW_MAX_TOKENS tokens with
+    bf16 activations; there are no counts, offsets, permutation, h or y then, and the result is closer to
+    the formula than the separate calls' (which round h and y), so not the same bits.
+
     capture(scores, x) records the forward into a HIP graph and replay() reruns it.
     """
 
     def __init__(self, T, H, I, E, k, experts, shared, score_fn="sigmoid", renorm=1, device="cuda",
-                 overlap_shared=True, act="bf16", fuse_shared="auto"):
+                 overlap_shared=True, act="bf16", fuse_shared="auto", few=False):
         if act not in ("bf16", "fp8"):
             raise ValueError(f"act must be 'bf16' or 'fp8', not {act!r}")
+        if few and act != "bf16":
+            raise ValueError("few=True takes bf16 activations")
         self.T, self.H, self.I, self.E, self.k = T, H, I, E, k
         self.act = act
         self.score_fn, self.renorm = score_fn, renorm
@@ -588,6 +595,13 @@ class MoeLayer:
         d, i32 = device, torch.int32
         self.topk_ids = torch.empty((T, k), dtype=i32, device=d)
         self.topk_w = torch.empty((T, k), dtype=torch.float32, device=d)
+        self.few = bool(few)
+        if self.few:
+            self.ws = torch.empty(max(16, moe_layer_few_workspace_size(T, k, self.w)),
+                                  dtype=torch.uint8, device=d)
+            self.out = torch.empty((max(1, T), H), dtype=torch.int16, device=d)
+            self.side = None
+            return
         self.counts = torch.empty(E, dtype=i32, device=d)
         self.offsets = torch.empty(E + 1, dtype=i32, device=d)
         self.perm = torch.empty(max(1, T * k), dtype=i32, device=d)
@@ -666,6 +680,12 @@ class MoeLayer:
         """Enqueue the layer; returns `out` (bf16 bits [T, H]).  gate_up_events=(start, stop)
         records torch events around the routed gate/up kernel (for timing; bf16 mode only)."""
         T, k = self.T, self.k
+        if self.few:
+            if gate_up_events is not None:
+                raise ValueError("few=True has no routed gate/up launch of its own")
+            moe_layer_few(scores, x, k, self.w, self.ws_, self.score_fn, self.renorm, self.topk_ids,
+                          self.topk_w, self.out[:T], self.ws, stream)
+            return self.out
         main = torch.cuda.current_stream() if stream is None else stream
         shared_y = None
         if self.ws_ is not None and self.side is not None:
@@ -701,6 +721,102 @@ class MoeLayer:
             main.wait_stream(self.side)
         moe_combine(self.y, self.inv, self.topk_w, shared_y, T, k, self.H, self.out, stream)
         return self.out
+
+
+class MoeBlock:
+    """Buffers and the call sequence of the second half of a transformer block whose feed-forward part is
+    a MoE layer:
+        s = hidden + residual;  n = RMS norm of s;  scores = n router_w^T;  out = the layer of n
+    moe_rmsnorm_quantize_act -> moe_router_scores -> MoeLayer, on the caller's stream (the layer's
+    shared expert as MoeLayer places it).  The next block's norm adds `out` to s.
+
+    `norm_w` is bf16 bits [H], `router_w` [E, H] bf16 bits or fp32; the other arguments are MoeLayer's.
+
+    act="fp8" with many rows per expert (T*k > 32*E, FP8 or MXFP4 weights, H a multiple of 256 and H and
+    I at most 8192): the gate/up GEMMs of the routed and the shared experts take the norm's own codes
+    (moe_expert_gate_up_a8), so that x is not read and quantised once more by each of them, and the codes
+    are those of the norm before its rounding to bf16.  Otherwise the layer quantises `normed` itself.
+
+    few="auto" (act="bf16") runs the layer as moe_layer_few wherever it takes the sizes; True / False
+    force it.
+
+    forward(hidden, residual) returns (out, s), capture(hidden, residual) records it into a HIP graph.
+    `residual` may be None (then s is hidden itself).
+    """
+
+    def __init__(self, T, H, I, E, k, norm_w, router_w, experts, shared, eps=1e-6,
+                 score_fn="sigmoid", renorm=1, device="cuda", act="bf16", few="auto"):
+        if few == "auto":
+            few = act == "bf16" and T <= FEW_MAX_TOKENS and T * (H + 8) <= FEW_MAX_X and k <= 32
+        self.layer = MoeLayer(T, H, I, E, k, experts, shared, score_fn, renorm, device, act=act, few=few)
+        self.T, self.H, self.E, self.k, self.eps = T, H, E, k, eps
+        self.norm_w, self.router_w = norm_w, router_w
+        d, b16 = device, torch.int16
+        self.sum = torch.empty((T, H), dtype=b16, device=d)
+        self.normed = torch.empty((T, H), dtype=b16, device=d)
+        self.scores = torch.empty((T, E), dtype=torch.float32, device=d)
+        self.router_ws = torch.empty(max(16, moe_router_scores_workspace_size(T, H, E)),
+                                     dtype=torch.uint8, device=d)
+        L = self.layer
+        self.codes = None
+        if (act == "fp8" and T * k > 32 * E and T > 32 and L.w.dtype != MOE_W_BF16 and H % 256 == 0
+                and H <= 8192 and I <= 8192 and (L.ws_ is None or L.ws_.dtype != MOE_W_BF16)):
+            def quantised(rows, K):
+                return (torch.empty((rows, K), dtype=torch.uint8, device=d),
+                        torch.empty((rows, exp_pitch(K)), dtype=torch.int8, device=d))
+            self.codes, self.exps = quantised(T, H)
+            self.h_q = quantised(T * k, I)
+            self.sh_q = quantised(T, I) if shared is not None else None
+
+    def _layer_a8(self, stream):
+        """The layer in the FP8 mode on the norm's codes, the shared expert on the layer's side stream."""
+        L, T, k = self.layer, self.T, self.k
+        main = torch.cuda.current_stream() if stream is None else stream
+        if L.side is not None:
+            L.side.wait_stream(main)
+            self._experts_a8(1, None, None, L.ws_, L.sh_h, self.sh_q, L.sh_y, L.side)
+        L._route_permute(self.scores, stream)
+        self._experts_a8(k, L.perm, L.offsets, L.w, L.h, self.h_q, L.y, stream)
+        if L.side is not None:
+            main.wait_stream(L.side)
+        moe_combine(L.y, L.inv, L.topk_w, L.sh_y if L.side is not None else None, T, k, self.H, L.out,
+                    stream)
+        return L.out
+
+    def _experts_a8(self, k, perm, offsets, w, h, h_q, y, stream):
+        moe_expert_gate_up_a8(self.codes, self.exps, k, perm, offsets, w, h, stream)
+        moe_quantize_act(h, *h_q, h_q[1].shape[1], stream)
+        moe_expert_down_a8(*h_q, self.T, k, offsets, w, y, stream)
+
+    def forward(self, hidden, residual=None, stream=None):
+        """Enqueue the block; returns (out, s), bf16 bits [T, H] (buffers of the block, `hidden` as s
+        without a residual)."""
+        a8 = self.codes is not None
+        moe_rmsnorm_quantize_act(hidden, self.norm_w, residual, self.eps, quantized=a8,
+                                 sum_out=None if residual is None else self.sum, y=self.normed,
+                                 codes=self.codes, exps=self.exps if a8 else None, stream=stream)
+        moe_router_scores(self.normed, self.router_w, self.scores, self.router_ws, stream)
+        out = self._layer_a8(stream) if a8 else self.layer.forward(self.scores, self.normed, stream)
+        return out[:self.T], hidden if residual is None else self.sum
+
+    def capture(self, hidden, residual=None):
+        """Record one forward on the tensors `hidden` and `residual` into a HIP graph; replay() reruns it
+        on whatever they hold then."""
+        warm = torch.cuda.Stream()
+        warm.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(warm):
+            self.forward(hidden, residual)
+        torch.cuda.current_stream().wait_stream(warm)
+        torch.cuda.synchronize()
+        self.graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(self.graph):
+            self._result = self.forward(hidden, residual)
+        return self.graph
+
+    def replay(self):
+        """Enqueue the captured forward on torch's current stream; returns (out, s)."""
+        self.graph.replay()
+        return self._result
 
 
 class MoeRankShare:

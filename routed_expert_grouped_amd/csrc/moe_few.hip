@@ -14,7 +14,8 @@
 // expert, so that the activations need no gather: in few_gate_up all eight tokens' rows are multiplied and
 // those not routed to the expert are not stored; in few_down a token's sum takes the experts that it
 // is routed to, by a select when the expert's blocks end (so that what a weight does to one token's sum
-// cannot reach another's).
+// cannot reach another's).  few_gate_up with MXFP4 weights takes the scaled 16x16x128 instruction instead:
+// weights and their scales as they are stored, x as two E4M3 codes in rows t and 8 + t (few_codes).
 //
 // h keeps fp32's precision: w_te * h_te goes on as two bf16 values, hi + lo (16 significand bits), in rows
 // t and 8 + t of the tile that eight tokens leave half empty, at no matrix instruction more.
@@ -23,9 +24,10 @@
 // units of 8 h columns (8 gate + 8 up rows); each wave streams its K part of unit after unit through a
 // ring of register stages that never drains between units, and the waves' sums meet in LDS once a
 // unit.  x (all tokens) stays in LDS, so that the ring's loads are weights alone: loads complete in
-// order, and a load of x behind them would wait for all of them.  The shared expert's unit comes first: its
-// loads are in flight while the routing runs.  few_down: a wave takes an even share of all (expert,
-// 128-block) stages of the workgroup's columns, and the waves' sums meet once at the end.
+// order, and a load of x behind them would wait for all of them.  The scores and x are loaded first, then
+// the shared expert's first unit, whose loads are in flight while the routing runs.  few_down: a wave takes
+// an even share of all (expert, 128-block) stages of the workgroup's columns, and the waves' sums meet once
+// at the end.
 #include "libmoe.h"
 #include "moe_device.h"
 #include "moe_ffn.h"
