@@ -215,12 +215,15 @@ __global__ __launch_bounds__(kLinWaves * 64) void linear_stream_kernel(LinArgs a
 // cores' time if they waited for each other), and its operands come from LDS.  So every wave runs three
 // things at once: subtile t's two products, subtile t - 1's multiply-adds between them, and the LDS reads
 // of later subtiles.  The last row of subtiles of a step reads the next step's first operands: the step's
-// barrier stands before it, when all of this step's operands are in registers (the loads of the step
-// after next go to the buffer that it frees) and the next step's have landed.
+// barrier stands before it, when all of this step's operands are in registers and the next step's have landed.
+// The loads of the step after next go to the buffer that it frees, over the four subtiles after the
+// barrier (two where a step has but four).
 template <int kMI, int kWM, int kWN>
 __global__ __launch_bounds__(kWM * kWN * 64) void linear_tile_kernel(LinArgs a) {
     constexpr int kNI = 2, kWaves = kWM * kWN, BM = 32 * kMI * kWM, BN = 32 * kNI * kWN;
     constexpr int kIA = BM / 8 / kWaves, kIB = BN / 8 / kWaves;  // direct loads a wave a step (8 rows each)
+    constexpr int kT = kMI * kNI;  // subtiles a step: even, so that subtile -1 is kT - 1 of the step before
+    static_assert(kT % 2 == 0, "p alternates over steps too");
     static_assert(kMI == 2 || kMI == 4, "the last row of subtiles follows the barrier");
     __shared__ __attribute__((aligned(1024))) uint8_t sA[2][BM * 128];
     __shared__ __attribute__((aligned(1024))) uint8_t sB[2][BN * 128];
@@ -232,23 +235,25 @@ __global__ __launch_bounds__(kWM * kWN * 64) void linear_tile_kernel(LinArgs a) 
     const int wm = wave / kWN, wn = wave % kWN, fr = lane & 31, half = lane >> 5;
     const int K = a.K, kb_all = K / 128, m0 = uniform(mt * BM), n0 = uniform(nt * BN);
 
-    // direct loads: from the tile's first row, at a byte offset per lane (rows past the end: the last row)
+    // direct loads, eight rows each: from their first row (the group of the last row for those past the
+    // end, whose products are not stored) at a byte offset per lane
+    constexpr int kLoads = kIA + kIB, kSlots = kT == 8 ? 4 : 2, kPart = kLoads / kSlots;
+    static_assert(kLoads == 8 && kIA % 2 == 0, "parts of whole loads; a load's parity is its row group's");
     const uint8_t *ab = a.a + (size_t)m0 * K, *bb = a.w + (size_t)n0 * K;
     const uint32_t la = lds_address(sA) + 8 * kIA * wave * 128, lb = lds_address(sB) + 8 * kIB * wave * 128;
-    auto issue = [&](int kb) {
+    const uint32_t lr = lane >> 3, lc = ((lane & 7) ^ (lane >> 4)) << 4;
+    auto issue = [&](int kb, auto tag) {  // loads part * kPart ... of step kb (past the end: of the last)
         const uint32_t buf = kb & 1;
-        // (the offsets are made here: eight registers held over a step would be eight too many)
-        int l = lane;
-        asm volatile("" : "+v"(l));
-        auto offset = [&](int r, int last) { return __umul24(min(r, last), K) + (((l & 7) ^ ((r >> 1) & 7)) << 4); };
+        const int at = min(kb, kb_all - 1) * 128;
 #pragma unroll
-        for (int i = 0; i < kIA; ++i)
-            lds_dma16_from(ab + (size_t)kb * 128, offset(8 * (kIA * wave + i) + (l >> 3), a.M - 1 - m0),
-                           la + buf * (BM * 128) + i * 1024);
-#pragma unroll
-        for (int i = 0; i < kIB; ++i)
-            lds_dma16_from(bb + (size_t)kb * 128, offset(8 * (kIB * wave + i) + (l >> 3), a.N - 1 - n0),
-                           lb + buf * (BN * 128) + i * 1024);
+        for (int l = decltype(tag)::value * kPart; l < decltype(tag)::value * kPart + kPart; ++l) {
+            const bool of_a = l < kIA;
+            const int i = of_a ? l : l - kIA, last = of_a ? a.M - 1 - m0 : a.N - 1 - n0;
+            const int row = min(8 * ((of_a ? kIA : kIB) * wave + i), last & ~7);
+            const uint32_t offset = __umul24(min(lr, (uint32_t)(last - row)), (uint32_t)K) + (lc ^ (64 * (i & 1)));
+            lds_dma16_from((of_a ? ab : bb) + (uint32_t)uniform(at + row * K), offset,
+                           (of_a ? la + buf * (BM * 128) : lb + buf * (BN * 128)) + i * 1024);
+        }
     };
     // the tile's scales, 16 blocks at a time in two buffers: E8M0 bytes of the rows, fp32 of the 128-column
     // groups (registers hold none of them over a step)
@@ -301,8 +306,6 @@ __global__ __launch_bounds__(kWM * kWN * 64) void linear_tile_kernel(LinArgs a) 
         // use, and hold every operand of the step in registers until then)
         asm volatile("" : "+v"(acc[t / kNI][t % kNI]));
     };
-    constexpr int kT = kMI * kNI;  // subtiles a step: even, so that subtile -1 is kT - 1 of the step before
-    static_assert(kT % 2 == 0, "p alternates over steps too");
     auto subtile = [&](auto tag, int kb) {
         constexpr int t = decltype(tag)::value, i = t / kNI, j = t % kNI;
         using prev = std::integral_constant<int, (t + kT - 1) % kT>;
@@ -315,6 +318,8 @@ __global__ __launch_bounds__(kWM * kWN * 64) void linear_tile_kernel(LinArgs a) 
         __builtin_amdgcn_sched_barrier(0);
         if constexpr (j == 0) read_e(next{}, kn);
         if constexpr (j == kNI - 1) read_a(next{}, 0, kn);
+        constexpr int slot = (t + kNI) % kT;  // subtiles since the barrier
+        if constexpr (slot < kSlots) issue(kb + 1 + (t >= kT - kNI), std::integral_constant<int, slot>{});
         take(prev{}, 0, scale);
         __builtin_amdgcn_sched_barrier(0);
         p[t & 1] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(fa[1], fb[j][1], p[t & 1], 0, 0, 0, ea[i & 1], 0, kLinE8M0One);
@@ -324,11 +329,11 @@ __global__ __launch_bounds__(kWM * kWN * 64) void linear_tile_kernel(LinArgs a) 
         take(prev{}, 8, scale);
         __builtin_amdgcn_sched_barrier(0);
     };
-    issue(0);
+    each_slot<kSlots>([&](auto tag) { issue(0, tag); });
     window(0);
     __builtin_amdgcn_s_waitcnt(vmcnt_imm(0));
     __syncthreads();
-    if (kb_all > 1) issue(1);
+    each_slot<2>([&](auto tag) { issue(1, tag); });  // (the other parts: in step 0)
     read_e(std::integral_constant<int, 0>{}, 0);
     read_a(std::integral_constant<int, 0>{}, 0, 0);
     read_a(std::integral_constant<int, 0>{}, 1, 0);
@@ -341,13 +346,13 @@ __global__ __launch_bounds__(kWM * kWN * 64) void linear_tile_kernel(LinArgs a) 
         // every wave has this step's operands in registers, and the next step's codes are in LDS
         __builtin_amdgcn_s_waitcnt(vmcnt_imm(0));
         __syncthreads();
-        if (kb + 2 < kb_all) issue(kb + 2);
         const float next = scale_of(kb + 1);
         subtile(std::integral_constant<int, kT - 2>{}, kb);
         subtile(std::integral_constant<int, kT - 1>{}, kb);
         sl = s;
         s = next;
     }
+    __builtin_amdgcn_s_waitcnt(vmcnt_imm(0));  // (no load may land after the workgroup's LDS is another's)
     take(std::integral_constant<int, kT - 1>{}, 0, sl);
     take(std::integral_constant<int, kT - 1>{}, 8, sl);
     // D layout: value v of a lane is row 8 (v / 4) + 4 half + v % 4, column fr
