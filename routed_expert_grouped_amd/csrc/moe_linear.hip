@@ -10,12 +10,12 @@
 // (zeros and subnormals too).
 //
 // Two shapes:
-//   stream  few rows: the weights' bytes bound it.  A workgroup owns 16 columns, its eight waves a part
-//           of K each, streamed through a ring of register stages (as in moe_few.hip); every weight
-//           stage meets 1, 2 or 4 tiles of 16 rows.  One 16x16x128 instruction is a whole 128-block.
-//   tile    many rows: the matrix cores bound it.  256 x 256 tiles (eight waves of 128 x 64), or 128 x 128
-//           (four waves of 64 x 64, two workgroups a CU) where the large ones would leave CUs idle.
-//           A K step is one 128-block, loaded directly to LDS in two buffers, one barrier a step.
+//   stream  few rows: the weights' bytes bound it.  A workgroup owns 16, 32 or 64 columns, its eight waves a
+//           part of K each, streamed through a ring of register stages (as in moe_few.hip); every
+//           weight stage meets 1, 2 or 4 tiles of 16 rows.  One 16x16x128 instruction is a whole 128-block.
+//   tile    many rows: the matrix cores bound it (8192^3: 2.34 PFLOP/s).  256 x 256 tiles (eight waves of 128 x
+//           64), or 128 x 128 (four waves of 64 x 64) where the large ones would leave CUs idle.
+//           A K step is one 128-block, loaded directly to LDS two or four steps deep, one barrier a step.
 // Rows and columns past the end read the last one's codes and are not stored, so every size takes the
 // same path.
 #include "libmoe.h"
@@ -205,7 +205,7 @@ __global__ __launch_bounds__(kLinWaves * 64) void linear_stream_kernel(LinArgs a
     }
 }
 
-// kMI x 2 subtiles of 32 x 32 a wave, kWM x kWN waves.
+// kMI x 2 subtiles of 32 x 32 a wave, kWM x kWN waves, kD steps (128 K each) in LDS.
 //
 // LDS rows are 128 bytes (one block's codes), eight 16-byte chunks, chunk c at slot c ^ ((row >> 1) & 7):
 // 16 consecutive rows' reads of one chunk fall in distinct banks.  32x32x64 operands: lane l holds row
@@ -218,15 +218,15 @@ __global__ __launch_bounds__(kLinWaves * 64) void linear_stream_kernel(LinArgs a
 // barrier stands before it, when all of this step's operands are in registers and the next step's have landed.
 // The loads of the step after next go to the buffer that it frees, over the four subtiles after the
 // barrier (two where a step has but four).
-template <int kMI, int kWM, int kWN>
+template <int kMI, int kWM, int kWN, int kD>
 __global__ __launch_bounds__(kWM * kWN * 64) void linear_tile_kernel(LinArgs a) {
     constexpr int kNI = 2, kWaves = kWM * kWN, BM = 32 * kMI * kWM, BN = 32 * kNI * kWN;
     constexpr int kIA = BM / 8 / kWaves, kIB = BN / 8 / kWaves;  // direct loads a wave a step (8 rows each)
     constexpr int kT = kMI * kNI;  // subtiles a step: even, so that subtile -1 is kT - 1 of the step before
     static_assert(kT % 2 == 0, "p alternates over steps too");
     static_assert(kMI == 2 || kMI == 4, "the last row of subtiles follows the barrier");
-    __shared__ __attribute__((aligned(1024))) uint8_t sA[2][BM * 128];
-    __shared__ __attribute__((aligned(1024))) uint8_t sB[2][BN * 128];
+    __shared__ __attribute__((aligned(1024))) uint8_t sA[kD][BM * 128];
+    __shared__ __attribute__((aligned(1024))) uint8_t sB[kD][BN * 128];
     __shared__ uint8_t sE[2][BM * 16];
     __shared__ float sS[2][BN / 128 * 16];
     int mt, nt;
@@ -243,7 +243,7 @@ __global__ __launch_bounds__(kWM * kWN * 64) void linear_tile_kernel(LinArgs a) 
     const uint32_t la = lds_address(sA) + 8 * kIA * wave * 128, lb = lds_address(sB) + 8 * kIB * wave * 128;
     const uint32_t lr = lane >> 3, lc = ((lane & 7) ^ (lane >> 4)) << 4;
     auto issue = [&](int kb, auto tag) {  // loads part * kPart ... of step kb (past the end: of the last)
-        const uint32_t buf = kb & 1;
+        const uint32_t buf = kb & (kD - 1);
         const int at = min(kb, kb_all - 1) * 128;
 #pragma unroll
         for (int l = decltype(tag)::value * kPart; l < decltype(tag)::value * kPart + kPart; ++l) {
@@ -279,12 +279,12 @@ __global__ __launch_bounds__(kWM * kWN * 64) void linear_tile_kernel(LinArgs a) 
     };
     auto read_a = [&](auto tag, int j, int kb) {
         constexpr int i = decltype(tag)::value;
-        fa[j] = frag(sA[kb & 1] + (wm * kMI + i) * 32 * 128, j);
+        fa[j] = frag(sA[kb & (kD - 1)] + (wm * kMI + i) * 32 * 128, j);
     };
     auto read_b = [&](auto tag, int kb) {
         constexpr int i = decltype(tag)::value;
 #pragma unroll
-        for (int j = 0; j < 2; ++j) fb[i][j] = frag(sB[kb & 1] + (wn * kNI + i) * 32 * 128, j);
+        for (int j = 0; j < 2; ++j) fb[i][j] = frag(sB[kb & (kD - 1)] + (wn * kNI + i) * 32 * 128, j);
     };
     auto scale_of = [&](int kb) { return sS[(kb >> 4) & 1][(wn * 32 * kNI / 128) * 16 + (kb & 15)]; };
     f32x16 acc[kMI][kNI], p[2];
@@ -319,7 +319,7 @@ __global__ __launch_bounds__(kWM * kWN * 64) void linear_tile_kernel(LinArgs a) 
         if constexpr (j == 0) read_e(next{}, kn);
         if constexpr (j == kNI - 1) read_a(next{}, 0, kn);
         constexpr int slot = (t + kNI) % kT;  // subtiles since the barrier
-        if constexpr (slot < kSlots) issue(kb + 1 + (t >= kT - kNI), std::integral_constant<int, slot>{});
+        if constexpr (slot < kSlots) issue(kb + kD - (t < kT - kNI), std::integral_constant<int, slot>{});
         take(prev{}, 0, scale);
         __builtin_amdgcn_sched_barrier(0);
         p[t & 1] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(fa[1], fb[j][1], p[t & 1], 0, 0, 0, ea[i & 1], 0, kLinE8M0One);
@@ -329,11 +329,12 @@ __global__ __launch_bounds__(kWM * kWN * 64) void linear_tile_kernel(LinArgs a) 
         take(prev{}, 8, scale);
         __builtin_amdgcn_sched_barrier(0);
     };
-    each_slot<kSlots>([&](auto tag) { issue(0, tag); });
     window(0);
-    __builtin_amdgcn_s_waitcnt(vmcnt_imm(0));
+#pragma unroll
+    for (int i = 0; i < kD - 1; ++i) each_slot<kSlots>([&](auto tag) { issue(i, tag); });
+    each_slot<2>([&](auto tag) { issue(kD - 1, tag); });  // (the other parts: in step 0)
+    __builtin_amdgcn_s_waitcnt(vmcnt_imm(kLoads * (kD - 2) + 2 * kPart));
     __syncthreads();
-    each_slot<2>([&](auto tag) { issue(1, tag); });  // (the other parts: in step 0)
     read_e(std::integral_constant<int, 0>{}, 0);
     read_a(std::integral_constant<int, 0>{}, 0, 0);
     read_a(std::integral_constant<int, 0>{}, 1, 0);
@@ -343,8 +344,9 @@ __global__ __launch_bounds__(kWM * kWN * 64) void linear_tile_kernel(LinArgs a) 
     for (int kb = 0; kb < kb_all; ++kb) {
         if ((kb & 15) == 8 && (kb | 15) + 1 < kb_all) window(kb / 16 + 1);
         each_slot<kT - kNI>([&](auto tag) { subtile(tag, kb); });
-        // every wave has this step's operands in registers, and the next step's codes are in LDS
-        __builtin_amdgcn_s_waitcnt(vmcnt_imm(0));
+        // every wave has this step's operands in registers, and the next step's codes are in LDS (the kD - 2
+        // steps after it may be in flight)
+        __builtin_amdgcn_s_waitcnt(vmcnt_imm(kLoads * (kD - 2)));
         __syncthreads();
         const float next = scale_of(kb + 1);
         subtile(std::integral_constant<int, kT - 2>{}, kb);
@@ -398,8 +400,10 @@ extern "C" moe_status moe_linear_a8(const uint8_t* x_codes, const int8_t* x_exps
     LinArgs a{x_codes, x_exps, exp_pitch, M, N, K, w, s_w, y, 0, 0};
     hipStream_t st = as_stream(stream);
     // Streaming or tiles, by the time each would take: the streaming kernel reads MT + kG tiles of 16 rows
-    // for every MT x kG of them (at the 7 TB/s that its loads come from the caches with), the tiles take
-    // 0.75 us a K step and round of 512 small ones.  Up to 64 rows always stream (the weights pass once).
+    // for every MT x kG of them (at the 7 TB/s that its loads come from the caches with), the small tiles
+    // take 0.75 us a K step where every CU has at most one, else 1.13 us a round of two.  Up to 64 rows always
+    // stream (the weights pass once).  128 x 7168 x 7168: 25 us streamed, 42 us in tiles; 256 x 7168 x
+    // 7168: 59 by that rule, 41 us in tiles.
     const int MT = M <= 16 ? 1 : M <= 32 ? 2 : 4;
     const int64_t rows = ((int64_t)M + 16 * MT - 1) / (16 * MT);
     const int64_t cols = ((int64_t)N + 15) / 16;
@@ -407,7 +411,7 @@ extern "C" moe_status moe_linear_a8(const uint8_t* x_codes, const int8_t* x_exps
     const int kG = rows * ((cols + 3) / 4) >= 192 ? 4 : rows * ((cols + 1) / 2) >= 192 ? 2 : 1;
     const double stream_us = (double)rows * ((cols + kG - 1) / kG) * (MT + kG) * 16 * K / 7e6;
     const int64_t small = ((int64_t)(M + 127) / 128) * ((N + 127) / 128);
-    const double tile_us = 0.75 * (K / 128) * ((small + 511) / 512);
+    const double tile_us = K / 128 * (small <= 256 ? 0.75 : 1.13 * ((small + 511) / 512));
     if (M <= 64 || (M <= 1024 && stream_us < tile_us)) {
 #define MOE_STREAM(T_, G_) \
     if (MT == T_ && kG == G_) return lin_launch(a, 16 * T_, 16 * G_, kLinWaves * 64, linear_stream_kernel<T_, G_>, st);
@@ -417,6 +421,9 @@ extern "C" moe_status moe_linear_a8(const uint8_t* x_codes, const int8_t* x_exps
 #undef MOE_STREAM
     }
     const int64_t large = ((int64_t)(M + 255) / 256) * ((N + 255) / 256);
-    if (large >= 192) return lin_launch(a, 256, 256, 512, linear_tile_kernel<4, 2, 4>, st);
-    return lin_launch(a, 128, 128, 256, linear_tile_kernel<2, 2, 2>, st);
+    if (large >= 192) return lin_launch(a, 256, 256, 512, linear_tile_kernel<4, 2, 4, 2>, st);
+    // four steps in LDS where a CU has one workgroup, else two for two of them (512 x 7168 x 7168, 224 tiles: 43
+    // us, with two steps 45; 1024 x 7168 x 7168, 448 tiles: two steps 63 us, four 86)
+    if (small <= 256) return lin_launch(a, 128, 128, 256, linear_tile_kernel<2, 2, 2, 4>, st);
+    return lin_launch(a, 128, 128, 256, linear_tile_kernel<2, 2, 2, 2>, st);
 }

@@ -20,6 +20,10 @@ SIZES = [  # M, N, K
     (257, 127, 384), (300, 2112, 256), (513, 129, 1152), (1000, 1000, 128), (3, 5, 65536), (129, 48, 18432),
     (300, 40, 16512),
     (3585, 3400, 256), (4000, 3333, 384),  # 256 x 256 tiles, ragged both ways
+    (3500, 3500, 2304),                    # ... and more than one window of scales
+    # 128 x 128 tiles, at most one a CU (1, 2, 3, 5 and 18 K steps) and two
+    (1100, 300, 128), (1030, 129, 256), (1100, 3000, 384), (1500, 700, 640), (1026, 200, 2304),
+    (1300, 3333, 1152), (2000, 2500, 128), (1025, 4200, 2304),
 ]
 
 
