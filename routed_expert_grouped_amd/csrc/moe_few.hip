@@ -529,12 +529,18 @@ __global__ __launch_bounds__(kFewThreads) void few_gate_up_kernel(FewArgs a) {
     });
 }
 
-// kG: 16-column groups of a workgroup
-template <int kFmt, int kG>
+// kG: 16-column groups of a workgroup; TT: at least T.  A stage's h rows, hi and lo of TT tokens, are loaded as
+// whole lines, 1024 / (2 kSV) rows an instruction, and go through LDS to the operand's layout.  (Loaded in
+// that layout, 64 chunks of 16 bytes an instruction whatever T is, the layer took 1 to 3% longer at 1 to 4
+// tokens, 7168 x 2048, MXFP4 the most; at 8 as long.)
+template <int kFmt, int kG, int TT>
 __global__ __launch_bounds__(kFewThreads) void few_down_kernel(FewArgs a) {
     using F = FewFmt<kFmt>;
-    constexpr int D = kFmt == kFewMX ? 3 : kFewRing;  // (an MXFP4 stage holds two blocks of h)
+    constexpr int D = kFmt == kFewMX && TT == 8 ? 3 : kFewRing;  // (an MXFP4 stage holds two blocks of h)
+    constexpr int kRowLanes = F::kSV / 8, kRows = 64 / kRowLanes;  // of an h load
+    constexpr int kHL = 2 * TT <= kRows ? 1 : 2 * TT / kRows, kHLD = 2 * F::kSV + 16;
     __shared__ __attribute__((aligned(16))) uint8_t sW[kFewWaves][16 * kFewLD];
+    __shared__ __attribute__((aligned(16))) uint8_t sH[kFewWaves][2 * TT * kHLD];
     __shared__ f32x4 red[kFewWaves][kG][kWave];
     __shared__ uint32_t list[kFewList + 1];
 
@@ -543,8 +549,11 @@ __global__ __launch_bounds__(kFewThreads) void few_down_kernel(FewArgs a) {
     const int T = a.T, H = a.H, I = a.I;
     const gbytes Wd = held(a.d), Xd = held(a.xd), Sd = held(a.sd), XSd = held(a.xsd), Hb = held(a.h);
     const int n0 = (int)blockIdx.x * 16 * kG;
+    // (entries past the count are loaded too, not to wait for it first; the head has room for all of them)
+    static_assert(kFewThreads >= kFewList + 1 && kFewHead >= (kFewList + 2) * sizeof(int32_t), "one entry a thread");
+    const uint32_t entry = (uint32_t)a.list[1 + min(tid, kFewList)];
     const int n_exp = uniform(a.list[0]);
-    for (int i = tid; i < n_exp; i += kFewThreads) list[i] = (uint32_t)a.list[1 + i];
+    if (tid <= kFewList) list[tid] = entry;
     __syncthreads();
     const int kb_all = I / 128, st_e = (I + F::kSV - 1) / F::kSV;  // stages of an expert
     const int S = n_exp * st_e;
@@ -553,24 +562,30 @@ __global__ __launch_bounds__(kFewThreads) void few_down_kernel(FewArgs a) {
     const int lrow = lane >> 3, lchunk = lane & 7;
     uint8_t* lds = sW[wave];
 
-    u32x4 bw[D][kG][2], hx[D][F::kNM];
+    u32x4 bw[D][kG][2], hx[D][kHL];
     float sc[D];
     uint32_t mx[D];
     int iu = 0, is = 0;       // issue cursor: list index, stage of the expert
     gbytes wp{}, hp{}, sp{};  // the expert's weight rows and h rows (uniform), this lane's scales
     const uint32_t wofs = (uint32_t)lrow * (uint32_t)row_bytes + lchunk * 16;  // this lane's bytes of a stage
-    uint32_t hofs = 0;        // this lane's h row, at its quarter
+    uint32_t hofs[kHL];       // this lane's chunks of the stage's h rows: row 2 t is token t's hi row, 2 t + 1 lo
+    auto hrow = [&](int j) { return (j * kRows + lane / kRowLanes) & (2 * TT - 1); };
+    uint8_t* hlds = sH[wave];
     auto expert_of = [&](int u) {
         const uint32_t entry = (uint32_t)uniform((int)list[u]);
         const int id = (int)(entry & 0xFFFF), mask = (int)(entry >> 16);
         const bool xg = id == kFewShared;
         const int e = xg ? 0 : id;
         wp = pick(xg, Xd, Wd) + ((size_t)e * H + n0) * row_bytes;
-        // rows of tokens that are not routed here hold nothing: such a lane reads another's row, and
-        // its sums are not taken
-        const int t = ((mask >> (m & 7)) & 1) ? (m & 7) : __ffs(mask) - 1;
         hp = Hb + 2 * (size_t)u * 2 * T * a.pitch;
-        hofs = 2 * ((uint32_t)(m < 8 ? t : T + t) * (uint32_t)a.pitch + F::value(0, kq));
+        // rows of tokens that are not routed here hold nothing: another's row is read, and its sums are not
+        // taken
+        const int any = __ffs(mask) - 1;
+#pragma unroll
+        for (int j = 0; j < kHL; ++j) {
+            const int r = hrow(j), t = (mask >> (r >> 1)) & 1 ? r >> 1 : any;
+            hofs[j] = 2 * (uint32_t)(t + (r & 1) * T) * (uint32_t)a.pitch + 16 * (lane & (kRowLanes - 1));
+        }
         const gbytes s = pick(xg, XSd, Sd);
         if (kFmt == kFewFP8) sp = s + 4 * ((size_t)e * (H / 128) + n0 / 128) * kb_all;
         if (kFmt == kFewMX) sp = s + ((size_t)e * H + n0 + mx_row(lane, kG)) * (I / 32);
@@ -587,8 +602,7 @@ __global__ __launch_bounds__(kFewThreads) void few_down_kernel(FewArgs a) {
                 bw[d][g][i] = __builtin_nontemporal_load(
                     (gvec<u32x4>)(wp + ((size_t)(16 * g + 8 * i) * row_bytes + (size_t)is * 128) + ofs));
 #pragma unroll
-        for (int i = 0; i < F::kNM; ++i)
-            hx[d][i] = *(gvec<u32x4>)(hp + (2 * is * F::kSV + 2 * F::value(i, 0)) + hofs);
+        for (int j = 0; j < kHL; ++j) hx[d][j] = *(gvec<u32x4>)(hp + 2 * is * F::kSV + hofs[j]);
         if (kFmt == kFewFP8) sc[d] = *(gvec<float>)(sp + 4 * is);
         if (kFmt == kFewMX) mx[d] = *(gvec<uint32_t>)(sp + 4 * min(kb + (lane & 1), kb_all - 1));
         if (--left > 0) {  // (past the wave's share its last stage is loaded again, into unused slots)
@@ -615,8 +629,15 @@ __global__ __launch_bounds__(kFewThreads) void few_down_kernel(FewArgs a) {
         });
         auto compute = [&](auto tag) {
             constexpr int d = decltype(tag)::value;
+#pragma unroll
+            for (int j = 0; j < kHL; ++j) *(u32x4*)&hlds[hrow(j) * kHLD + 16 * (lane & (kRowLanes - 1))] = hx[d][j];
+            __builtin_amdgcn_wave_barrier();
+            const uint8_t* hm = hlds + (2 * min(m & 7, TT - 1) + (m >> 3)) * kHLD + 2 * F::value(0, kq);
+            bf16x8 xv[F::kNM];
+#pragma unroll
+            for (int i = 0; i < F::kNM; ++i) xv[i] = as_bf16x8(*(const u32x4*)&hm[2 * F::value(i, 0)]);
             few_stage<kFmt, kG>(lds, bw[d], lane, kFmt == kFewMX ? mx[d] : 0u, kFmt == kFewFP8 ? sc[d] : 0.0f,
-                                [&](int i) { return as_bf16x8(hx[d][i]); }, pe);
+                                [&](int i) { return xv[i]; }, pe);
         };
         auto flush = [&]() {  // the expert's sums, for the tokens routed to it (a wave's share may
                               // begin or end inside an expert)
@@ -687,8 +708,14 @@ static moe_status launch_few(const FewArgs& a, hipStream_t st) {
     const moe_status s = launch_status();
     if (s != MOE_OK) return s;
     // 32 columns a workgroup where that leaves at least 7 of 8 CUs one, else 16
-    if (a.H / 32 >= 224) few_down_kernel<kFmt, 2><<<dim3((unsigned)(a.H / 32)), dim3(kFewThreads), 0, st>>>(a);
-    else few_down_kernel<kFmt, 1><<<dim3((unsigned)(a.H / 16)), dim3(kFewThreads), 0, st>>>(a);
+    auto down = [&](auto tag) {
+        constexpr int TT = decltype(tag)::value;
+        if (a.H / 32 >= 224) few_down_kernel<kFmt, 2, TT><<<dim3((unsigned)(a.H / 32)), block, 0, st>>>(a);
+        else few_down_kernel<kFmt, 1, TT><<<dim3((unsigned)(a.H / 16)), block, 0, st>>>(a);
+    };
+    if (a.T <= 2) down(std::integral_constant<int, 2>{});
+    else if (a.T <= 4) down(std::integral_constant<int, 4>{});
+    else down(std::integral_constant<int, 8>{});
     return launch_status();
 }
 
