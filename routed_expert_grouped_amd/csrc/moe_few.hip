@@ -27,7 +27,7 @@
 // order, and a load of x behind them would wait for all of them.  The scores and x are loaded first, then
 // the shared expert's first unit, whose loads are in flight while the routing runs.  few_down: a wave takes
 // an even share of all (expert, 128-block) stages of the workgroup's columns, and the waves' sums meet once
-// at the end.
+// at the end; where the columns alone leave CUs idle, several workgroups share the stages of a tile.
 #include "libmoe.h"
 #include "moe_device.h"
 #include "moe_ffn.h"
@@ -47,8 +47,10 @@ constexpr int kFewXBytes = 114816;   // LDS for x: 8 rows of 7168 bf16, padded b
 constexpr int kFewCodeBytes = kFewXBytes + 16 * kFewT;  // ... or 16 of codes, as many more
 constexpr int kFewList = kFewT * MOE_MAX_TOPK;  // most touched experts
 constexpr int kFewShared = 0xFFFF;   // the shared expert's id in the list
-constexpr size_t kFewHead = 2048;    // workspace: list (count, then id | token mask << 16), then h
-static_assert((kFewList + 2) * sizeof(int32_t) <= kFewHead, "the list fits the workspace's head");
+constexpr int kFewParts = 8;         // most workgroups of a few_down tile
+// workspace: list (count, then id | token mask << 16), arrivals of few_down's tiles, h, their parts' sums
+constexpr size_t kFewCounts = 2048, kFewHead = kFewCounts + MOE_MAX_DIM / 32 * sizeof(int32_t);
+static_assert((kFewList + 2) * sizeof(int32_t) <= kFewCounts, "the list fits before the arrivals");
 
 struct FewArgs {
     const float* scores;
@@ -63,6 +65,9 @@ struct FewArgs {
     int32_t* list;
     uint16_t* h;  // [list index][2 T][pitch]: hi rows 0..T-1, lo rows T..2T-1
     int pitch;    // I rounded up to 256 (two blocks), the rest zeros
+    int down_g, parts;  // few_down: 16-column groups of a tile, workgroups of a tile
+    int32_t* arrived;   // [tile]
+    float* part;        // [part][tile][group][8][16]
     uint16_t* out;
 };
 
@@ -419,6 +424,8 @@ __global__ __launch_bounds__(kFewThreads) void few_gate_up_kernel(FewArgs a) {
         for (int i = tid; i < n_exp; i += kFewThreads)
             a.list[1 + i] = i < sh ? (int32_t)(kFewShared | ((1u << T) - 1) << 16) : (int32_t)list[i - sh];
         if (tid == 0) a.list[0] = n_exp;
+        if (a.parts > 1)
+            for (int i = tid; i < H / 32; i += kFewThreads) a.arrived[i] = 0;
     }
     if ((int)blockIdx.x >= n_units) return;  // (whole workgroups)
     if (ns > 0) {
@@ -543,12 +550,14 @@ __global__ __launch_bounds__(kFewThreads) void few_down_kernel(FewArgs a) {
     __shared__ __attribute__((aligned(16))) uint8_t sH[kFewWaves][2 * TT * kHLD];
     __shared__ f32x4 red[kFewWaves][kG][kWave];
     __shared__ uint32_t list[kFewList + 1];
+    __shared__ int before;
 
     const int tid = (int)threadIdx.x, lane = lane_id(), wave = uniform(tid >> 6);
     const int m = lane & 15, kq = lane >> 4;
     const int T = a.T, H = a.H, I = a.I;
     const gbytes Wd = held(a.d), Xd = held(a.xd), Sd = held(a.sd), XSd = held(a.xsd), Hb = held(a.h);
-    const int n0 = (int)blockIdx.x * 16 * kG;
+    const int tiles = H / (16 * kG), my_part = (int)blockIdx.x / tiles, tile = (int)blockIdx.x - my_part * tiles;
+    const int n0 = tile * 16 * kG;
     // (entries past the count are loaded too, not to wait for it first; the head has room for all of them)
     static_assert(kFewThreads >= kFewList + 1 && kFewHead >= (kFewList + 2) * sizeof(int32_t), "one entry a thread");
     const uint32_t entry = (uint32_t)a.list[1 + min(tid, kFewList)];
@@ -557,7 +566,8 @@ __global__ __launch_bounds__(kFewThreads) void few_down_kernel(FewArgs a) {
     __syncthreads();
     const int kb_all = I / 128, st_e = (I + F::kSV - 1) / F::kSV;  // stages of an expert
     const int S = n_exp * st_e;
-    const int q0 = (int)((int64_t)S * wave / kFewWaves), q1 = (int)((int64_t)S * (wave + 1) / kFewWaves);
+    const int share = my_part * kFewWaves + wave, shares = a.parts * kFewWaves;
+    const int q0 = (int)((int64_t)S * share / shares), q1 = (int)((int64_t)S * (share + 1) / shares);
     const size_t row_bytes = F::row_bytes(I);
     const int lrow = lane >> 3, lchunk = lane & 7;
     uint8_t* lds = sW[wave];
@@ -666,15 +676,48 @@ __global__ __launch_bounds__(kFewThreads) void few_down_kernel(FewArgs a) {
 #pragma unroll
     for (int g = 0; g < kG; ++g) red[wave][g][lane] = acc[g];
     __syncthreads();
-    if (wave < kG) {  // wave g joins group g, in wave order, and adds the lo rows to the hi rows
-        f32x4 v = red[0][wave][lane];
+    // wave g joins group g, in wave order, and adds the lo rows to the hi rows: value r is column m of token
+    // 4 kq + r (lanes 0..31)
+    f32x4 v{};
+    if (wave < kG) {
+        v = red[0][wave][lane];
 #pragma unroll
         for (int w = 1; w < kFewWaves; ++w) v += red[w][wave][lane];
 #pragma unroll
+        for (int r = 0; r < 4; ++r) v[r] += __shfl(v[r], lane | 32, kWave);
+    }
+    const bool mine = wave < kG && lane < 32;
+    if (a.parts > 1) {
+        // The tile's workgroups leave their sums in memory, past the XCDs' caches (agent scope); the one that
+        // arrives last adds them all, in part order.  A sum is there before its arrival is counted: the
+        // stores are waited for.
+        const auto at = [&](int p, int r) {
+            return a.part + ((((size_t)p * tiles + tile) * kG + wave) * kFewT + 4 * kq + r) * 16 + m;
+        };
+        if (mine) {
+#pragma unroll
+            for (int r = 0; r < 4; ++r) __hip_atomic_store(at(my_part, r), v[r], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        }
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        __syncthreads();
+        if (tid == 0) before = __hip_atomic_fetch_add(&a.arrived[tile], 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        __syncthreads();
+        if (before != a.parts - 1 || !mine) return;
+        f32x4 p[kFewParts];
+#pragma unroll
+        for (int i = 0; i < kFewParts; ++i)
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                p[i][r] = i < a.parts ? __hip_atomic_load(at(i, r), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) : 0.0f;
+        v = p[0];
+#pragma unroll
+        for (int i = 1; i < kFewParts; ++i) v += p[i];
+    }
+    if (mine) {
+#pragma unroll
         for (int r = 0; r < 4; ++r) {
-            const float lo = __shfl(v[r], lane | 32, kWave);
             const int t = 4 * kq + r;
-            if (lane < 32 && t < T) a.out[(size_t)t * H + n0 + 16 * wave + m] = f32_to_bf16(v[r] + lo);
+            if (t < T) a.out[(size_t)t * H + n0 + 16 * wave + m] = f32_to_bf16(v[r]);
         }
     }
 }
@@ -691,9 +734,52 @@ static moe_status check_few(int32_t T, int32_t k, const moe_expert_weights* w) {
 
 static int few_pitch(int I) { return (I + 255) & ~255; }
 
+// few_down's tiles and the workgroups that share one, by the time each choice would take: a round of the chip's
+// CUs costs 4 us before its loads arrive, a workgroup streams at most the rate below (the chip 6.8 KB/ns), and
+// a join costs 3 us.  Measured, us a layer (groups x parts; the rule's choice marked):
+//   2048 x 1408, FP8, 8 tokens     1x1 84   2x1 98   2x2 78   2x4 69*  2x8 73
+//   4096 x 1536, MXFP4, 8 tokens   1x1 112  2x1 123  2x2 102* 2x4 107  2x8 118
+//   5120 x 1536, FP8, 8 tokens     1x1 237  2x1 212  2x2 221  2x3 202* 2x8 214
+//   7168 x 2048, MXFP4, 1 token    1x1 50   2x1 46*  2x2 53   2x8 75
+struct FewDown {
+    int g, parts;
+};
+static FewDown few_down_plan(int64_t experts, int H, int fmt, double row_bytes) {
+    static const double rate[3][2] = {{33, 42}, {24, 36}, {14, 21}};  // bytes/ns: bf16, FP8, MXFP4; one group, two
+    FewDown best{1, 1};
+    double best_ns = 1e30;
+    for (int g : {1, 2})
+        for (int parts = 1; parts <= (g == 2 ? kFewParts : 1); ++parts) {
+            const int groups = H / (16 * g) * parts, rounds = (groups + 255) / 256;
+            const double bytes = 16.0 * g * (double)experts * row_bytes / parts;  // of a workgroup
+            const double ns = 4000.0 * rounds + std::max(rounds * bytes / rate[fmt][g - 1], groups * bytes / 6800.0) +
+                              (parts > 1 ? 3000.0 : 0.0);
+            if (ns < best_ns) best_ns = ns, best = {g, parts};
+        }
+    return best;
+}
+
+static int64_t few_experts(int T, int k, const moe_expert_weights* w) {  // the most there can be, and the shared one
+    return std::min<int64_t>((int64_t)T * k, w->n_groups) + 1;
+}
+
+static FewDown few_down_of(int T, int k, const moe_expert_weights* w) {
+    const int64_t experts = few_experts(T, k, w);
+    switch (w->dtype) {
+        case MOE_W_BF16: return few_down_plan(experts, w->H, kFewBF16, 2.0 * w->I);
+        case MOE_W_FP8_E4M3_B128: return few_down_plan(experts, w->H, kFewFP8, w->I);
+        default: return few_down_plan(experts, w->H, kFewMX, w->I * 17.0 / 32);
+    }
+}
+
+static size_t few_h_bytes(int T, int k, const moe_expert_weights* w) {
+    return few_experts(T, k, w) * 2 * T * (size_t)few_pitch(w->I) * sizeof(uint16_t);
+}
+
 static size_t few_ws(int T, int k, const moe_expert_weights* w) {
-    const size_t experts = std::min<int64_t>((int64_t)T * k, w->n_groups) + 1;  // and the shared one
-    return T == 0 ? 0 : kFewHead + experts * 2 * T * (size_t)few_pitch(w->I) * sizeof(uint16_t);
+    if (T == 0) return 0;
+    const int parts = few_down_of(T, k, w).parts;
+    return kFewHead + few_h_bytes(T, k, w) + (parts > 1 ? (size_t)parts * kFewT * w->H * sizeof(float) : 0);
 }
 
 template <int kFmt>
@@ -707,11 +793,11 @@ static moe_status launch_few(const FewArgs& a, hipStream_t st) {
     else few_gate_up_kernel<kFmt, 1><<<grid, block, 0, st>>>(a);
     const moe_status s = launch_status();
     if (s != MOE_OK) return s;
-    // 32 columns a workgroup where that leaves at least 7 of 8 CUs one, else 16
     auto down = [&](auto tag) {
         constexpr int TT = decltype(tag)::value;
-        if (a.H / 32 >= 224) few_down_kernel<kFmt, 2, TT><<<dim3((unsigned)(a.H / 32)), block, 0, st>>>(a);
-        else few_down_kernel<kFmt, 1, TT><<<dim3((unsigned)(a.H / 16)), block, 0, st>>>(a);
+        const dim3 grid((unsigned)(a.H / (16 * a.down_g) * a.parts));
+        if (a.down_g == 2) few_down_kernel<kFmt, 2, TT><<<grid, block, 0, st>>>(a);
+        else few_down_kernel<kFmt, 1, TT><<<grid, block, 0, st>>>(a);
     };
     if (a.T <= 2) down(std::integral_constant<int, 2>{});
     else if (a.T <= 4) down(std::integral_constant<int, 4>{});
@@ -766,6 +852,10 @@ extern "C" moe_status moe_layer_few(const float* scores, const uint16_t* x, int3
     a.list = static_cast<int32_t*>(ws);
     a.h = reinterpret_cast<uint16_t*>(static_cast<uint8_t*>(ws) + kFewHead);
     a.pitch = few_pitch(w->I);
+    const FewDown down = few_down_of(T, k, w);
+    a.down_g = down.g, a.parts = down.parts;
+    a.arrived = reinterpret_cast<int32_t*>(static_cast<uint8_t*>(ws) + kFewCounts);
+    a.part = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + kFewHead + few_h_bytes(T, k, w));
     a.out = out;
     hipStream_t st = as_stream(stream);
     switch (w->dtype) {

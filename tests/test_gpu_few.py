@@ -61,6 +61,9 @@ SHAPES = [  # T, H, I, E, k
     (2, 16384, 128, 4, 2),
     (3, 16384, 384, 6, 3),
     (1, 2048, 7168, 3, 2),
+    # several workgroups a tile of the down phase (and shares of them without a stage)
+    (8, 1024, 512, 40, 8), (4, 2048, 1408, 16, 6), (8, 4096, 640, 24, 6), (8, 5120, 512, 30, 8),
+    (2, 2048, 1408, 8, 8), (8, 256, 2048, 48, 8),
 ]
 
 
@@ -255,3 +258,38 @@ def test_no_tokens_and_refusals():
     with pytest.raises(moe.MoeError) as e:
         moe.moe_layer_few(layer.scores, layer.x, 2, w, ws, work=torch.empty(16, dtype=torch.uint8, device=DEV))
     assert e.value.status == moe.MOE_ERR_WORKSPACE
+
+
+@pytest.mark.parametrize("wdtype", ["fp8", "bf16", "mxfp4"])
+def test_shared_tiles_give_equal_bits_every_time(wdtype):
+    """Several workgroups add to a tile of the down phase, in an order that must not show: eager, with any
+    workspace contents, on two streams at once, and replayed."""
+    layer = make(8, 1024, 512, 40, 8, wdtype, seed=12)
+    w, ws = moe.expert_weights(layer.experts), moe.expert_weights(layer.shared)
+    works = [torch.empty(moe.moe_layer_few_workspace_size(8, 8, w), dtype=torch.uint8, device=DEV) for _ in range(2)]
+    outs = [torch.empty((8, 1024), dtype=torch.int16, device=DEV) for _ in range(2)]
+    want = run(layer)[0].clone()
+
+    def call(i, **kw):
+        moe.moe_layer_few(layer.scores, layer.x, 8, w, ws, layer.score_fn, layer.renorm, out=outs[i], work=works[i], **kw)
+    for fill in (0, 1, 255, None, None):
+        if fill is not None:
+            works[0].fill_(fill)
+        call(0)
+        assert torch.equal(outs[0], want)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for i in range(2):
+            call(i, stream=streams[i])
+    torch.cuda.synchronize()
+    assert torch.equal(outs[0], want) and torch.equal(outs[1], want)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call(0)
+    for _ in range(5):
+        outs[0].zero_()
+        works[0].fill_(170)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(outs[0], want)
