@@ -28,6 +28,11 @@
 // the shared expert's first unit, whose loads are in flight while the routing runs.  few_down: a wave takes
 // an even share of all (expert, 128-block) stages of the workgroup's columns, and the waves' sums meet once
 // at the end; where the columns alone leave CUs idle, several workgroups share the stages of a tile.
+//
+// Measured, 7168 x 2048, 256 experts, top-8 and a shared expert: 1 token 67 us FP8 (gate/up 45, down 23; the
+// weights alone 58 at 6.8 TB/s), 46 us MXFP4, 125 us bf16; 8 tokens 367 to 392 us FP8, 234 to 248 us MXFP4 (gate/up
+// 147 to 156 at 6.2 TB/s, down 88 to 93: bound by the instructions that expand 4-bit weights).  4 x 256 x 128:
+// 10 us, two dependent launches of 5.7 and 3.9.
 #include "libmoe.h"
 #include "moe_device.h"
 #include "moe_ffn.h"

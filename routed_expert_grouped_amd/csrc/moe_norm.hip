@@ -15,6 +15,9 @@
 // Lane layout: chunk c of a row is its values 8c .. 8c + 7 (16 bytes); thread i owns chunks i,
 // i + threads, ...  With a workgroup of whole waves a 128-block is 16 consecutive lanes, whose maximum
 // is taken by DPP without LDS.
+//
+// Bound by HBM at many rows: 32768 x 7168 with everything on 374 us, 5.7 TB/s of reads and writes together (a
+// copy of torch's reaches 4.8, a read alone 6.8).  One row: 3.5 us, the latency of load, sum and store.
 #include "libmoe.h"
 #include "moe_device.h"
 #include "moe_host.h"
