@@ -367,8 +367,8 @@ moe_status moe_router_scores_workspace_size(int32_t T, int32_t H, int32_t E, siz
  *            aligned (may be NULL when that size is 0), not used by other work until the enqueued
  *            launches complete.
  * Errors: INVALID_ARG for T < 0, H < 1, E < 1, an unknown w_dtype, null or unaligned pointers;
- * UNSUPPORTED when H is not a multiple of 8, H > MOE_MAX_DIM, E > MOE_MAX_EXPERTS or T*E >= 2^31;
- * WORKSPACE when ws is NULL or too small. */
+ * UNSUPPORTED when H is not a multiple of 8, H > MOE_MAX_DIM, E > MOE_MAX_EXPERTS, T > 2^29 or
+ * T*E >= 2^31; WORKSPACE when ws is NULL or too small. */
 moe_status moe_router_scores(const uint16_t* x, int32_t T, int32_t H, const void* w,
                              int32_t w_dtype, int32_t E, float* scores, void* ws, size_t ws_bytes,
                              void* stream);

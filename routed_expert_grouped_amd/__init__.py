@@ -600,7 +600,7 @@ class MoeLayer:
             self.ws = torch.empty(max(16, moe_layer_few_workspace_size(T, k, self.w)),
                                   dtype=torch.uint8, device=d)
             self.out = torch.empty((max(1, T), H), dtype=torch.int16, device=d)
-            self.side = None
+            self.side, self.fused = None, False
             return
         self.counts = torch.empty(E, dtype=i32, device=d)
         self.offsets = torch.empty(E + 1, dtype=i32, device=d)

@@ -377,9 +377,9 @@ __global__ __launch_bounds__(kWM * kWN * 64) void linear_tile_kernel(LinArgs a) 
 
 template <typename F>
 static moe_status lin_launch(LinArgs a, int BM, int BN, int threads, F kernel, hipStream_t st) {
-    a.m_tiles = (a.M + BM - 1) / BM;
-    a.n_tiles = (a.N + BN - 1) / BN;
-    const int64_t R = (int64_t)a.m_tiles * a.n_tiles;
+    const int64_t mt = ((int64_t)a.M + BM - 1) / BM, nt = ((int64_t)a.N + BN - 1) / BN, R = mt * nt;
+    a.m_tiles = (int)mt;
+    a.n_tiles = (int)nt;
     if (R > (1 << 22)) return MOE_ERR_UNSUPPORTED;  // (a launch holds fewer than 2^32 threads)
     kernel<<<dim3((unsigned)((R + 7) / 8 * 8)), dim3(threads), 0, st>>>(a);
     return launch_status();
@@ -412,7 +412,7 @@ extern "C" moe_status moe_linear_a8(const uint8_t* x_codes, const int8_t* x_exps
     // as many column groups a workgroup as leave one for most CUs
     const int kG = rows * ((cols + 3) / 4) >= 192 ? 4 : rows * ((cols + 1) / 2) >= 192 ? 2 : 1;
     const double stream_us = (double)rows * ((cols + kG - 1) / kG) * (MT + kG) * 16 * K / 7e6;
-    const int64_t small = ((int64_t)(M + 127) / 128) * ((N + 127) / 128);
+    const int64_t small = (((int64_t)M + 127) / 128) * (((int64_t)N + 127) / 128);
     const double tile_us = K / 128 * (small <= 256 ? 0.75 : 1.13 * ((small + 511) / 512));
     if (M <= 64 || (M <= 1024 && stream_us < tile_us)) {
 #define MOE_STREAM(T_, G_) \
@@ -422,7 +422,7 @@ extern "C" moe_status moe_linear_a8(const uint8_t* x_codes, const int8_t* x_exps
         MOE_STREAM(4, 1) MOE_STREAM(4, 2) MOE_STREAM(4, 4)
 #undef MOE_STREAM
     }
-    const int64_t large = ((int64_t)(M + 255) / 256) * ((N + 255) / 256);
+    const int64_t large = (((int64_t)M + 255) / 256) * (((int64_t)N + 255) / 256);
     if (large >= 192) return lin_launch(a, 256, 256, 512, linear_tile_kernel<4, 2, 4, 2>, st);
     // four steps in LDS where a CU has one workgroup, else two for two of them (512 x 7168 x 7168, 224 tiles: 43
     // us, with two steps 45; 1024 x 7168 x 7168, 448 tiles: two steps 63 us, four 86)

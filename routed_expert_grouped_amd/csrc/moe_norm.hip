@@ -46,7 +46,7 @@ __global__ __launch_bounds__(kNormMaxThreads) void rmsnorm_kernel(
         gv[i] = c < chunks ? *(const u32x4*)(g + 8 * c) : u32x4{0u, 0u, 0u, 0u};
     }
     int parity = 0;
-    for (int row = (int)blockIdx.x; row < rows; row += (int)gridDim.x, parity ^= 1) {
+    for (int64_t row = blockIdx.x; row < rows; row += gridDim.x, parity ^= 1) {
         const size_t at = (size_t)row * K;
         u32x4 xv[V], rv[V];
 #pragma unroll

@@ -444,7 +444,7 @@ static RouterPlan router_plan(int T, int H, int E, bool f32) {
         }
     }
     p.n_tiles = (E + p.kN - 1) / p.kN;
-    p.tiles = (T + p.kM - 1) / p.kM * p.n_tiles;
+    p.tiles = (int)(((int64_t)T + p.kM - 1) / p.kM) * p.n_tiles;
     // one round of workgroups (two a CU of the small tiles), at least four K steps each
     const int steps = (H + kRtK - 1) / kRtK;
     p.splits = std::max(1, std::min((p.dma ? 256 : 512) / p.tiles, steps / 4));
@@ -457,7 +457,8 @@ static moe_status check_router(int32_t T, int32_t H, int32_t E, int32_t w_dtype)
     if (T < 0 || H < 1 || E < 1) return MOE_ERR_INVALID_ARG;
     if (w_dtype != MOE_ROUTER_W_BF16 && w_dtype != MOE_ROUTER_W_F32) return MOE_ERR_INVALID_ARG;
     if (H % 8 != 0 || H > MOE_MAX_DIM || E > MOE_MAX_EXPERTS) return MOE_ERR_UNSUPPORTED;
-    if ((int64_t)T * E > INT32_MAX) return MOE_ERR_UNSUPPORTED;
+    // (a launch holds fewer than 2^32 threads, 512 for 128 rows)
+    if ((int64_t)T * E > INT32_MAX || T > 1 << 29) return MOE_ERR_UNSUPPORTED;
     return MOE_OK;
 }
 

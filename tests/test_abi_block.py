@@ -41,7 +41,8 @@ def test_router():
     for bad in (dict(x=None), dict(w=None), dict(out=None), dict(T=-1), dict(H=0), dict(E=0), dict(dt=2),
                 dict(dt=-1), dict(x=ODD), dict(w=ODD), dict(out=ODD)):
         assert router(**bad) == INV, bad
-    for bad in (dict(H=100), dict(H=16384 + 8), dict(E=1025), dict(T=1 << 24, E=1024)):
+    for bad in (dict(H=100), dict(H=16384 + 8), dict(E=1025), dict(T=1 << 24, E=1024),
+                dict(T=(1 << 31) - 1, H=8, E=1)):
         assert router(**bad) == UNS, bad
     need = moe.moe_router_scores_workspace_size(100, 7168, 64)
     assert need % (100 * 64 * 4) == 0 and need > 0
@@ -99,7 +100,9 @@ def test_linear():
     for bad in (dict(a=None), dict(e=None), dict(w=None), dict(s=None), dict(y=None), dict(M=-1), dict(N=0),
                 dict(K=0), dict(pitch=1), dict(a=ODD), dict(e=ODD), dict(w=ODD), dict(s=ODD), dict(y=ODD)):
         assert linear(**bad) == INV, bad
-    for bad in (dict(K=100), dict(K=65536 + 128, pitch=1024), dict(M=1 << 30, N=1 << 20)):
+    for bad in (dict(K=100), dict(K=65536 + 128, pitch=1024), dict(M=1 << 30, N=1 << 20),
+                dict(M=(1 << 31) - 1, N=1 << 20), dict(M=1 << 20, N=(1 << 31) - 1),
+                dict(M=(1 << 31) - 1, N=(1 << 31) - 1), dict(M=1, N=(1 << 31) - 1)):
         assert linear(**bad) == UNS, bad
 
 
