@@ -25,6 +25,7 @@
 #include "moe_device.h"
 #include "moe_host.h"
 #include "moe_lds.h"
+#include "moe_ring.h"
 
 #include <algorithm>
 
@@ -92,21 +93,23 @@ __global__ __launch_bounds__(kDotThreads) void router_dot_kernel(const uint16_t*
     }
 }
 
-// The three bf16 parts of two floats (a in the low halves): an infinity or a NaN is all in the first.
+// The three bf16 parts of two floats (a in the low halves), each the upper half of what is left: cut off, not
+// rounded, so that the next difference is exact and has eight significant bits less.  An infinity is all in the
+// first part; a NaN whose first part is an infinity has a NaN as its second.
 __device__ __forceinline__ void split3(float a, float b, uint32_t* parts) {
-#pragma unroll
-    for (int p = 0; p < 3; ++p) {
-        const uint32_t v = f32x2_to_bf16x2(a, b);
-        parts[p] = v;
-        const float ha = __uint_as_float(v << 16), hb = __uint_as_float(v & 0xffff0000u);
-        a = isfinite(ha) ? a - ha : 0.0f;
-        b = isfinite(hb) ? b - hb : 0.0f;
-    }
+    const auto upper = [](float v) { return __uint_as_float(__float_as_uint(v) & 0xffff0000u); };
+    const auto pack = [](float lo, float hi) { return __builtin_amdgcn_perm(__float_as_uint(hi), __float_as_uint(lo), 0x07060302u); };
+    const float ah = upper(a), bh = upper(b);
+    parts[0] = pack(a, b);
+    a = a == ah ? 0.0f : a - ah;
+    b = b == bh ? 0.0f : b - bh;
+    parts[1] = pack(a, b);
+    parts[2] = pack(a - upper(a), b - upper(b));
 }
 
-// 64 x 64 tile, four waves of 32 x 32, K in steps of 64.  The next step's operands are loaded to registers
-// before the current step's products and written to the other LDS buffer after them, one barrier a step
-// (fp32 W: one buffer of three planes, two barriers).
+// 64 x 64 tile, four waves of 32 x 32, K in steps of 64 through two LDS buffers (fp32 W: three planes), one
+// barrier a step.  With K split over the chip a workgroup has but a few steps, so latency is what they cost:
+// the operands of four steps are in flight in registers.
 constexpr int kRtK = 64;
 constexpr int kRtLd = kRtK * 2 + 16;  // LDS row bytes: 16 consecutive rows' 16-byte reads hit distinct banks
 
@@ -114,11 +117,10 @@ template <bool kF32>
 __global__ __launch_bounds__(256) void router_gemm_kernel(const uint16_t* __restrict__ x, int T, int H,
                                                           const void* __restrict__ w, int E, int n_tiles,
                                                           int tiles, int splits, float* __restrict__ out) {
-    constexpr int kMI = 1, kNI = 1;
-    constexpr int kPlanes = kF32 ? 3 : 1, kBufs = kF32 ? 1 : 2, kM = 64 * kMI, kN = 64 * kNI;
-    constexpr int kLA = kM / 32, kLB = kN / 32, kWB = kF32 ? 2 : 1;  // staging loads a thread, 16-byte words of 8 weights
-    __shared__ __attribute__((aligned(16))) uint8_t sA[kBufs][kM * kRtLd];
-    __shared__ __attribute__((aligned(16))) uint8_t sB[kBufs][kPlanes][kN * kRtLd];
+    constexpr int kPlanes = kF32 ? 3 : 1, kWB = kF32 ? 2 : 1;  // (16-byte words of 8 weights)
+    constexpr int kM = 64, kN = 64, kL = kM / 32, D = 4;       // staging loads a thread and operand, steps in flight
+    __shared__ __attribute__((aligned(16))) uint8_t sA[2][kM * kRtLd];
+    __shared__ __attribute__((aligned(16))) uint8_t sB[2][kPlanes][kN * kRtLd];
     // consecutive workgroups go to the 8 XCDs in turn: XCD i takes the contiguous range i of logical
     // tiles, so that the column tiles of a row tile share its x rows in one L2
     const int R8 = (tiles * splits + 7) / 8;
@@ -132,100 +134,90 @@ __global__ __launch_bounds__(256) void router_gemm_kernel(const uint16_t* __rest
     const int tid = (int)threadIdx.x, lane = lane_id(), wave = tid / kWave;
     const int wm = wave >> 1, wn = wave & 1, fr = lane & 31, half = lane >> 5;
     // staging: thread loads 16-byte chunk tid % 8 of rows tid / 8 + 32 i; rows past the end read the last
-    // row (not stored), chunks past H are zeros (both operands: 0 times garbage could be NaN)
+    // row (not stored), chunks past H the last chunk, and are staged as zeros (both operands: 0 times garbage
+    // could be NaN)
     const int lc = tid & 7, lr = tid >> 3;
-    u32x4 ra[kLA], rb[kLB][kWB];
-    auto load = [&](int step) {
-        const int c = step * (kRtK / 8) + lc;
-        const bool in = c < H / 8;
+    const uint16_t* xr[kL];
+    const char* wr[kL];
 #pragma unroll
-        for (int i = 0; i < kLA; ++i)
-            ra[i] = in ? ((const u32x4*)(x + (size_t)min(m0 + lr + 32 * i, T - 1) * H))[c] : u32x4{0u, 0u, 0u, 0u};
+    for (int i = 0; i < kL; ++i) {
+        xr[i] = x + (size_t)min(m0 + lr + 32 * i, T - 1) * H;
+        wr[i] = (const char*)w + (size_t)min(n0 + lr + 32 * i, E - 1) * H * (kF32 ? 4 : 2);
+    }
+    u32x4 ra[D][kL], rb[D][kL][kWB];
+    auto load = [&](auto tag, int step) {
+        constexpr int d = decltype(tag)::value;
+        const int c = min(step * (kRtK / 8) + lc, H / 8 - 1);
 #pragma unroll
-        for (int i = 0; i < kLB; ++i) {
-            const char* row = (const char*)w + (size_t)min(n0 + lr + 32 * i, E - 1) * H * (kF32 ? 4 : 2);
+        for (int i = 0; i < kL; ++i) ra[d][i] = ((const u32x4*)xr[i])[c];
 #pragma unroll
-            for (int p = 0; p < kWB; ++p)
-                rb[i][p] = in ? ((const u32x4*)row)[kWB * c + p] : u32x4{0u, 0u, 0u, 0u};
-        }
+        for (int i = 0; i < kL; ++i)
+#pragma unroll
+            for (int p = 0; p < kWB; ++p) rb[d][i][p] = ((const u32x4*)wr[i])[kWB * c + p];
     };
-    auto stage = [&](int buf) {
+    auto stage = [&](auto tag, int buf, int step) {
+        constexpr int d = decltype(tag)::value;
+        const uint32_t keep = step * (kRtK / 8) + lc < H / 8 ? 0xFFFFFFFFu : 0u;
 #pragma unroll
-        for (int i = 0; i < kLA; ++i) *(u32x4*)&sA[buf][(lr + 32 * i) * kRtLd + lc * 16] = ra[i];
+        for (int i = 0; i < kL; ++i) *(u32x4*)&sA[buf][(lr + 32 * i) * kRtLd + lc * 16] = ra[d][i] & keep;
 #pragma unroll
-        for (int i = 0; i < kLB; ++i) {
+        for (int i = 0; i < kL; ++i) {
             const int at = (lr + 32 * i) * kRtLd + lc * 16;
             if constexpr (kF32) {
                 u32x4 pl[3];
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     uint32_t q[3];
-                    split3(__uint_as_float(rb[i][j >> 1][(2 * j) & 3]), __uint_as_float(rb[i][j >> 1][(2 * j + 1) & 3]), q);
+                    split3(__uint_as_float(rb[d][i][j >> 1][(2 * j) & 3] & keep),
+                           __uint_as_float(rb[d][i][j >> 1][(2 * j + 1) & 3] & keep), q);
 #pragma unroll
                     for (int p = 0; p < 3; ++p) pl[p][j] = q[p];
                 }
 #pragma unroll
                 for (int p = 0; p < 3; ++p) *(u32x4*)&sB[buf][p][at] = pl[p];
             } else {
-                *(u32x4*)&sB[buf][0][at] = rb[i][0];
+                *(u32x4*)&sB[buf][0][at] = rb[d][i][0] & keep;
             }
         }
     };
-    f32x16 acc[kMI][kNI];
+    f32x16 acc;
 #pragma unroll
-    for (int i = 0; i < kMI; ++i)
-#pragma unroll
-        for (int j = 0; j < kNI; ++j)
-#pragma unroll
-            for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.0f;
+    for (int v = 0; v < 16; ++v) acc[v] = 0.0f;
     auto compute = [&](int buf) {
 #pragma unroll
         for (int ks = 0; ks < kRtK / 16; ++ks) {
-            bf16x8 fa[kMI];
-#pragma unroll
-            for (int i = 0; i < kMI; ++i)
-                fa[i] = as_bf16x8(*(const u32x4*)&sA[buf][((wm * kMI + i) * 32 + fr) * kRtLd + ks * 32 + half * 16]);
+            const bf16x8 fa = as_bf16x8(*(const u32x4*)&sA[buf][(wm * 32 + fr) * kRtLd + ks * 32 + half * 16]);
 #pragma unroll
             for (int p = kPlanes - 1; p >= 0; --p) {  // the small parts first
-                bf16x8 fb[kNI];
-#pragma unroll
-                for (int j = 0; j < kNI; ++j)
-                    fb[j] = as_bf16x8(*(const u32x4*)&sB[buf][p][((wn * kNI + j) * 32 + fr) * kRtLd + ks * 32 + half * 16]);
-#pragma unroll
-                for (int i = 0; i < kMI; ++i)
-#pragma unroll
-                    for (int j = 0; j < kNI; ++j)
-                        acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fa[i], fb[j], acc[i][j], 0, 0, 0);
+                const bf16x8 fb = as_bf16x8(*(const u32x4*)&sB[buf][p][(wn * 32 + fr) * kRtLd + ks * 32 + half * 16]);
+                acc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fa, fb, acc, 0, 0, 0);
             }
         }
     };
-    load(k0);
-    stage(0);
-    __syncthreads();
-    for (int s = k0; s < k1; ++s) {
-        const int buf = kBufs == 2 ? (s - k0) & 1 : 0;
-        if (s + 1 < k1) load(s + 1);
-        compute(buf);
-        if (s + 1 < k1) {
-            if (kBufs == 1) __syncthreads();
-            stage(kBufs == 2 ? buf ^ 1 : 0);
-        }
+    // (in slot order, as the loop has them: the waits count on it; past the end the last step is loaded again)
+    each_slot<D>([&](auto tag) {
+        load(tag, min(k0 + decltype(tag)::value, k1 - 1));
+        __builtin_amdgcn_sched_barrier(0);
+    });
+    int s = k0;
+    ring_loop<D>(k1 - k0, [&](auto tag) {
+        const int buf = (s - k0) & 1;  // (its readers of two steps ago have passed the last step's barrier)
+        stage(tag, buf, s);
+        __builtin_amdgcn_sched_barrier(0);
+        load(tag, min(s + D, k1 - 1));
+        __builtin_amdgcn_sched_barrier(0);
         __syncthreads();
-    }
+        compute(buf);
+        ++s;
+    });
     // D layout: value v of a lane is row 8 (v / 4) + 4 half + v % 4, column fr
     float* o = out + (size_t)split * T * E;
+    const int e = n0 + wn * 32 + fr;
 #pragma unroll
-    for (int i = 0; i < kMI; ++i)
-#pragma unroll
-        for (int v = 0; v < 16; ++v) {
-            const int t = m0 + (wm * kMI + i) * 32 + 8 * (v >> 2) + 4 * half + (v & 3);
-            if (t >= T) continue;
-#pragma unroll
-            for (int j = 0; j < kNI; ++j) {
-                const int e = n0 + (wn * kNI + j) * 32 + fr;
-                if (e < E) o[(size_t)t * E + e] = acc[i][j][v];
-            }
-        }
+    for (int v = 0; v < 16; ++v) {
+        const int t = m0 + wm * 32 + 8 * (v >> 2) + 4 * half + (v & 3);
+        if (t < T && e < E) o[(size_t)t * E + e] = acc[v];
+    }
 }
 
 // fp32 W to its three bf16 parts [3][E][H]

@@ -81,6 +81,24 @@ def test_nan_and_infinity_stay_in_their_row_or_column(T):
     assert torch.equal(got[rows, 5], sign * float("inf"))
 
 
+@pytest.mark.parametrize("T", [5, 40, 2100])
+def test_fp32_weights_of_every_kind(T):
+    """Weights of both signs down to 2^-100, infinities and NaNs of any payload: rows that pick one return it."""
+    H, E = 128, 16
+    gen = rng(T)
+    w = randn(gen, E, H) * torch.exp2(torch.randint(-100, 100, (E, H), generator=gen).float())
+    pick = torch.randint(0, H, (T,), generator=gen)
+    x = torch.zeros(T, H)
+    x[torch.arange(T), pick] = 1.0
+    assert torch.equal(call(bits(x), w, T, E), w[:, pick].T.double())
+    w[0, 3], w[1, 5], w[2, 7] = float("inf"), float("-inf"), float("nan")
+    w.view(torch.int32)[3, 9] = 0x7F800001  # a NaN whose upper half is an infinity's
+    x = torch.ones(T, H)
+    got = call(bits(x), w, T, E)
+    assert bool((got[:, 0] == float("inf")).all() and (got[:, 1] == float("-inf")).all())
+    assert bool(torch.isnan(got[:, 2:4]).all() and torch.isfinite(got[:, 4:]).all())
+
+
 def test_sums_in_the_same_order_every_time():
     gen = rng(1)
     x, w = bits(randn(gen, 700, 7168)).to(DEV), bits(randn(gen, 256, 7168)).to(DEV)
