@@ -10,9 +10,9 @@
 //               sums are joined in a fixed order.  W's bytes and the launch bound it.
 //   more        tiles on the matrix cores (32x32x16 bf16), operands through LDS.  When the tiles alone
 //               do not fill the chip, K is split over workgroups into fp32 partial scores in the
-//               caller's workspace, and a second launch adds them in order.  Up to a few thousand tokens
-//               64 x 64 tiles staged through registers; above, tiles of 128 x 256, 192 or 128 loaded directly
-//               to LDS, three stages deep.
+//               caller's workspace, and a second launch adds them in order.  Small batches take
+//               64 x 64 tiles staged through registers, large ones tiles of 128 x 256, 192 or 128 loaded
+//               directly to LDS, three stages deep.
 //
 // Measured, 7168 values a row, 256 experts, bf16 W: 1 token 6 us (the call), 512 tokens 13 us, 8192 tokens 46 us
 // (663 TFLOP/s), 32768 tokens 144 to 147 us (837 TFLOP/s, 3.3 TB/s of x: loads to LDS and matrix cores bound it
@@ -419,11 +419,13 @@ struct RouterPlan {
     size_t w_bytes, part_bytes;  // workspace: fp32 W's parts, then the partial scores
 };
 
-constexpr int kRouterDmaT = 2048;
+// From so many 64 x 64 tiles on the large ones are faster (2048 x 7168 x 256, 128 tiles: 21 us against 28; 3000 x
+// 7168 x 256, 188 tiles: 31 against 28; 1500 x 7168 x 384, 144 tiles: 24 against 22)
+constexpr int kRouterDmaTiles = 148;
 
 static RouterPlan router_plan(int T, int H, int E, bool f32) {
     RouterPlan p{};
-    p.dma = T >= kRouterDmaT;
+    p.dma = ((int64_t)T + 63) / 64 * ((E + 63) / 64) >= kRouterDmaTiles;
     p.kM = p.dma ? 128 : 64;
     // of 256, 192 and 128 columns the width that loads the fewest rows, kN of W and 128 of x a tile
     // (32768 x 7168 x 384: 192 columns 203 us, 128 columns 229)

@@ -17,9 +17,11 @@ SIZES = [  # T, H, E: both kernels, ragged tiles, K tails, split and unsplit
     (1, 8, 1), (1, 7168, 256), (2, 256, 7), (3, 520, 16), (4, 1024, 64), (5, 2048, 129), (8, 7168, 384),
     (9, 264, 33), (16, 7168, 256), (17, 7168, 256), (31, 8, 5), (64, 72, 130), (127, 512, 128),
     (128, 1032, 129), (129, 2048, 255), (333, 7168, 384), (1000, 640, 1024), (4096, 512, 256),
-    # the large batches' tiles: one and several K steps, none that is whole, a last one of one chunk, both widths
+    # around and above the large batches' tiles: one and several K steps, none that is whole, a last one of one chunk, both widths
     (2048, 64, 256), (2049, 8, 5), (2047, 72, 130), (2048, 72, 130), (2100, 1032, 384), (2300, 120, 300),
     (2048, 7168, 256), (2177, 2056, 1000), (5000, 192, 256), (2200, 1160, 100), (2050, 4096, 192),
+    (10000, 8, 5), (9500, 64, 33), (9473, 72, 16), (5000, 1160, 100), (3300, 4096, 192), (2432, 64, 256),
+    (2560, 7168, 256),
 ]
 
 
@@ -53,7 +55,7 @@ def test_whole_numbers_are_exact(T, H, E, f32):
     assert torch.equal(got, x.double() @ w.double().T)
 
 
-@pytest.mark.parametrize("T", [1, 5, 16, 17, 300, 2500])
+@pytest.mark.parametrize("T", [1, 5, 16, 17, 300, 2500, 10000])
 def test_every_bit_of_an_fp32_weight_counts(T):
     """Rows that pick one weight each return it bit for bit."""
     H, E = 256, 40
@@ -65,7 +67,7 @@ def test_every_bit_of_an_fp32_weight_counts(T):
     assert torch.equal(call(bits(x), w, T, E), w[:, pick].T.double())
 
 
-@pytest.mark.parametrize("T", [4, 16, 40, 2100])
+@pytest.mark.parametrize("T", [4, 16, 40, 2100, 9500])
 def test_nan_and_infinity_stay_in_their_row_or_column(T):
     H, E = 328, 48
     gen = rng(T)
@@ -81,7 +83,7 @@ def test_nan_and_infinity_stay_in_their_row_or_column(T):
     assert torch.equal(got[rows, 5], sign * float("inf"))
 
 
-@pytest.mark.parametrize("T", [5, 40, 2100])
+@pytest.mark.parametrize("T", [5, 40, 2100, 9500])
 def test_fp32_weights_of_every_kind(T):
     """Weights of both signs down to 2^-100, infinities and NaNs of any payload: rows that pick one return it."""
     H, E = 128, 16
@@ -128,7 +130,7 @@ def test_no_tokens():
     assert moe.moe_router_scores(x, w).shape == (0, 8)
 
 
-@pytest.mark.parametrize("T", [3, 200, 2048])
+@pytest.mark.parametrize("T", [3, 200, 2048, 2500])
 def test_streams_and_graph(T):
     gen = rng(T)
     x, w = bits(randn(gen, T, 2048)).to(DEV), bits(randn(gen, 256, 2048)).to(DEV)
