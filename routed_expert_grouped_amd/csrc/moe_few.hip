@@ -541,18 +541,20 @@ __global__ __launch_bounds__(kFewThreads) void few_gate_up_kernel(FewArgs a) {
     });
 }
 
-// kG: 16-column groups of a workgroup; TT: at least T.  A stage's h rows, hi and lo of TT tokens, are loaded as
-// whole lines, 1024 / (2 kSV) rows an instruction, and go through LDS to the operand's layout.  (Loaded in
-// that layout, 64 chunks of 16 bytes an instruction whatever T is, the layer took 1 to 3% longer at 1 to 4
-// tokens, 7168 x 2048, MXFP4 the most; at 8 as long.)
+// kG: 16-column groups of a workgroup; TT: at least T.  Up to four tokens a stage's h rows, hi and lo of TT
+// tokens, are loaded as whole lines, 1024 / (2 kSV) rows an instruction, and go through LDS to the operand's
+// layout; eight fill that layout's 16 rows, and are loaded in it.  (7168 x 2048, MXFP4: the layer of 1 to 4 tokens
+// took 2 to 3% longer the other way, FP8 and bf16 1%; of 8 tokens this phase took 98 us against 93.)
 template <int kFmt, int kG, int TT>
 __global__ __launch_bounds__(kFewThreads) void few_down_kernel(FewArgs a) {
     using F = FewFmt<kFmt>;
     constexpr int D = kFmt == kFewMX && TT == 8 ? 3 : kFewRing;  // (an MXFP4 stage holds two blocks of h)
     constexpr int kRowLanes = F::kSV / 8, kRows = 64 / kRowLanes;  // of an h load
-    constexpr int kHL = 2 * TT <= kRows ? 1 : 2 * TT / kRows, kHLD = 2 * F::kSV + 16;
+    constexpr bool kDirect = TT == 8;
+    constexpr int kHL = kDirect ? F::kNM : 2 * TT <= kRows ? 1 : 2 * TT / kRows, kHLD = 2 * F::kSV + 16;
+    constexpr int kHO = kDirect ? 1 : kHL;  // offsets a lane
     __shared__ __attribute__((aligned(16))) uint8_t sW[kFewWaves][16 * kFewLD];
-    __shared__ __attribute__((aligned(16))) uint8_t sH[kFewWaves][2 * TT * kHLD];
+    __shared__ __attribute__((aligned(16))) uint8_t sH[kFewWaves][kDirect ? 16 : 2 * TT * kHLD];
     __shared__ f32x4 red[kFewWaves][kG][kWave];
     __shared__ uint32_t list[kFewList + 1];
     __shared__ int before;
@@ -583,8 +585,8 @@ __global__ __launch_bounds__(kFewThreads) void few_down_kernel(FewArgs a) {
     int iu = 0, is = 0;       // issue cursor: list index, stage of the expert
     gbytes wp{}, hp{}, sp{};  // the expert's weight rows and h rows (uniform), this lane's scales
     const uint32_t wofs = (uint32_t)lrow * (uint32_t)row_bytes + lchunk * 16;  // this lane's bytes of a stage
-    uint32_t hofs[kHL];       // this lane's chunks of the stage's h rows: row 2 t is token t's hi row, 2 t + 1 lo
-    auto hrow = [&](int j) { return (j * kRows + lane / kRowLanes) & (2 * TT - 1); };
+    uint32_t hofs[kHO];       // this lane's chunks of the stage's h rows: row 2 t is token t's hi row, 2 t + 1 lo
+    auto hrow = [&](int j) { return kDirect ? 2 * (m & 7) + (m >> 3) : (j * kRows + lane / kRowLanes) & (2 * TT - 1); };
     uint8_t* hlds = sH[wave];
     auto expert_of = [&](int u) {
         const uint32_t entry = (uint32_t)uniform((int)list[u]);
@@ -597,9 +599,9 @@ __global__ __launch_bounds__(kFewThreads) void few_down_kernel(FewArgs a) {
         // taken
         const int any = __ffs(mask) - 1;
 #pragma unroll
-        for (int j = 0; j < kHL; ++j) {
+        for (int j = 0; j < kHO; ++j) {
             const int r = hrow(j), t = (mask >> (r >> 1)) & 1 ? r >> 1 : any;
-            hofs[j] = 2 * (uint32_t)(t + (r & 1) * T) * (uint32_t)a.pitch + 16 * (lane & (kRowLanes - 1));
+            hofs[j] = 2 * (uint32_t)(t + (r & 1) * T) * (uint32_t)a.pitch + (kDirect ? 2 * F::value(0, kq) : 16 * (lane & (kRowLanes - 1)));
         }
         const gbytes s = pick(xg, XSd, Sd);
         if (kFmt == kFewFP8) sp = s + 4 * ((size_t)e * (H / 128) + n0 / 128) * kb_all;
@@ -617,7 +619,7 @@ __global__ __launch_bounds__(kFewThreads) void few_down_kernel(FewArgs a) {
                 bw[d][g][i] = __builtin_nontemporal_load(
                     (gvec<u32x4>)(wp + ((size_t)(16 * g + 8 * i) * row_bytes + (size_t)is * 128) + ofs));
 #pragma unroll
-        for (int j = 0; j < kHL; ++j) hx[d][j] = *(gvec<u32x4>)(hp + 2 * is * F::kSV + hofs[j]);
+        for (int j = 0; j < kHL; ++j) hx[d][j] = *(gvec<u32x4>)(hp + (2 * is * F::kSV + (kDirect ? 2 * F::value(j, 0) : 0)) + hofs[kDirect ? 0 : j]);
         if (kFmt == kFewFP8) sc[d] = *(gvec<float>)(sp + 4 * is);
         if (kFmt == kFewMX) mx[d] = *(gvec<uint32_t>)(sp + 4 * min(kb + (lane & 1), kb_all - 1));
         if (--left > 0) {  // (past the wave's share its last stage is loaded again, into unused slots)
@@ -644,13 +646,18 @@ __global__ __launch_bounds__(kFewThreads) void few_down_kernel(FewArgs a) {
         });
         auto compute = [&](auto tag) {
             constexpr int d = decltype(tag)::value;
-#pragma unroll
-            for (int j = 0; j < kHL; ++j) *(u32x4*)&hlds[hrow(j) * kHLD + 16 * (lane & (kRowLanes - 1))] = hx[d][j];
-            __builtin_amdgcn_wave_barrier();
-            const uint8_t* hm = hlds + (2 * min(m & 7, TT - 1) + (m >> 3)) * kHLD + 2 * F::value(0, kq);
             bf16x8 xv[F::kNM];
+            if constexpr (kDirect) {
 #pragma unroll
-            for (int i = 0; i < F::kNM; ++i) xv[i] = as_bf16x8(*(const u32x4*)&hm[2 * F::value(i, 0)]);
+                for (int i = 0; i < F::kNM; ++i) xv[i] = as_bf16x8(hx[d][i]);
+            } else {
+#pragma unroll
+                for (int j = 0; j < kHL; ++j) *(u32x4*)&hlds[hrow(j) * kHLD + 16 * (lane & (kRowLanes - 1))] = hx[d][j];
+                __builtin_amdgcn_wave_barrier();
+                const uint8_t* hm = hlds + (2 * min(m & 7, TT - 1) + (m >> 3)) * kHLD + 2 * F::value(0, kq);
+#pragma unroll
+                for (int i = 0; i < F::kNM; ++i) xv[i] = as_bf16x8(*(const u32x4*)&hm[2 * F::value(i, 0)]);
+            }
             few_stage<kFmt, kG>(lds, bw[d], lane, kFmt == kFewMX ? mx[d] : 0u, kFmt == kFewFP8 ? sc[d] : 0.0f,
                                 [&](int i) { return xv[i]; }, pe);
         };
