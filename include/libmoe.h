@@ -353,8 +353,9 @@ moe_status moe_rmsnorm_quantize_act(const uint16_t* x, const uint16_t* residual,
 typedef enum { MOE_ROUTER_W_BF16 = 0, MOE_ROUTER_W_F32 = 1 } moe_router_wdtype;
 
 /* Bytes of device workspace moe_router_scores needs (host output; the larger of both weight types): 0 up to
- * 16 tokens and where the output tiles alone fill the chip, else fp32 partial scores of the parts
- * K is split into.  Errors as for moe_router_scores, plus INVALID_ARG for a null `bytes`. */
+ * 16 tokens, else the fp32 partial scores of the parts K is split into where the output tiles alone
+ * do not fill the chip, and for large batches fp32 W's three bf16 parts.  Errors as for moe_router_scores,
+ * plus INVALID_ARG for a null `bytes`. */
 moe_status moe_router_scores_workspace_size(int32_t T, int32_t H, int32_t E, size_t* bytes);
 
 /* Router scores: scores[t][e] = sum_h x[t][h] w[e][h], products exact, sums in fp32, in an order
