@@ -16,8 +16,8 @@
 //   tile    many rows: the matrix cores bound it (8192^3: 2.34 PFLOP/s).  256 x 256 tiles (eight waves of 128 x
 //           64), or 128 x 128 (four waves of 64 x 64) where the large ones would leave CUs idle.
 //           A K step is one 128-block, loaded directly to LDS two or four steps deep, one barrier a step.
-// Measured, N = K = 7168: 1 row 11 us, 16 rows 12 us, 64 rows 20 us, 512 rows 43 us, 1024 rows 63 us, 4096 rows 204
-// to 234 us (1.8 to 2.07 PFLOP/s: 448 tiles are 1.75 rounds of the CUs).
+// Measured, N = K = 7168: 1 row 11 us, 16 rows 12 us, 64 rows 20 us, 512 rows 43 us, 1024 rows 63 us, 4096 rows 195
+// to 234 us (1.8 to 2.15 PFLOP/s: 448 tiles are 1.75 rounds of the CUs).
 // Rows and columns past the end read the last one's codes and are not stored, so every size takes the
 // same path.
 #include "libmoe.h"

@@ -15,7 +15,7 @@
 //               directly to LDS, three stages deep.
 //
 // Measured, 7168 values a row, 256 experts, bf16 W: 1 token 6 us (the call), 512 tokens 13 us, 8192 tokens 46 us
-// (663 TFLOP/s), 32768 tokens 144 to 147 us (837 TFLOP/s, 3.3 TB/s of x: loads to LDS and matrix cores bound it
+// (663 TFLOP/s), 32768 tokens 140 to 147 us (837 TFLOP/s, 3.3 TB/s of x: loads to LDS and matrix cores bound it
 // together); fp32 W at 32768 tokens 362 us (1.0 PFLOP/s of bf16 products).
 //
 // fp32 W goes to the matrix cores as three bf16 parts, w = hi + mid + lo (8 + 8 + 8 significand bits:
